@@ -109,6 +109,7 @@ typedef enum { SPECV_F32 = 0, SPECV_BF16 = 1 } specv_dtype;
 #define SPECV_MAX_GAMMA 31      /* one 64-bit status word holds a row's accept and stop bits */
 #define SPECV_MAX_TOP_K 1024
 #define SPECV_MAX_VOCAB 524288
+#define SPECV_MAX_RECORD_K 256  /* tokens of a teacher's record (specv_top_logits)       */
 
 typedef struct {
     int device;      /* HIP device ordinal the handle runs on                     */
@@ -315,6 +316,199 @@ SPECV_API specv_status specv_verify_greedy(specv_handle h, void* stream,
                                  int32_t eos_id,
                                  int32_t* out_num_accepted, int32_t* out_tokens,
                                  int32_t* out_num_emitted, int32_t* out_row_flags);
+
+/* ------------------------------------------------------------------------
+ * Logits operators around a round.  Before it: specv_adjust_logits applies
+ * penalties for repeated tokens, biases and grammar masks to the target or
+ * draft rows ("11.1 核心原理" 11.1.2: p_i and q_i are taken after each
+ * model's constraints), with the token history kept by specv_history_add and
+ * specv_history_reset.  After it: specv_top_logits turns the target rows into
+ * a teacher's record, and the specv_distill_* calls give the loss of a
+ * drafter against it and its gradient ("投机解码 Speculative Decoding"
+ * tutorial, section 4.2: distilling the draft model toward the target).
+ *
+ * Rows are [B, n_pos, V] as above.  These calls use nothing of the handle's
+ * workspace: B and n_pos are not bound by max_batch and max_gamma (V is by
+ * max_vocab), any number of them may run at once, and next to a verify call
+ * on the same handle; the handle gives the device and, with profiling on
+ * (then calls must not overlap), the events.  They are captured and replayed
+ * as they are.  The calling thread's current device is restored on return.
+ * Rows of any element-aligned address are taken.  Output rows must not
+ * overlap each other, and an output may be its input (same address and
+ * strides) where stated but must not overlap it otherwise (SPECV_E_SHAPE).
+ * ------------------------------------------------------------------------ */
+
+/* Per-row penalties of specv_adjust_logits, device array [B] (16 bytes each,
+ * 16-byte aligned). */
+typedef struct {
+    float repetition;   /* r > 0: a used token's logit z becomes z / r if z > 0, else z * r; 1: off */
+    float presence;     /* a: subtracted once from the logits of generated tokens; 0: off          */
+    float frequency;    /* f: subtracted per occurrence of a generated token; 0: off               */
+    int32_t slot;       /* the row's history; outside [0, n_slots): an empty history               */
+} specv_penalties;
+
+/* What specv_adjust_logits applies (host struct of device pointers; a NULL
+ * penalties, bias_offsets or mask leaves that step out). */
+typedef struct {
+    const specv_penalties* penalties; /* [B]                                                      */
+    const int32_t* counts;            /* [n_slots, V]: occurrences among the generated tokens      */
+    const uint32_t* seen;             /* [n_slots, W], W = ceil(V / 32): bit v % 32 of word v / 32
+                                         is set when token v is in the prompt or was generated
+                                         (a token whose count is not 0 has its bit set)            */
+    int32_t n_slots;                  /* 0: empty histories (counts and seen may be NULL)          */
+    const int32_t* draft_tokens;      /* [B, >= pos0 + n_pos - 1] the round's drafts, which count as
+                                         generated at the positions behind them; NULL: none        */
+    int64_t token_stride;             /* entries per batch row of draft_tokens                     */
+    const int32_t* bias_offsets;      /* [B + 1]: row b's entries are bias_offsets[b] ..
+                                         bias_offsets[b + 1] - 1 (cut to [0, n_bias))              */
+    const int32_t* bias_tokens;       /* [n_bias]; entries outside [0, V) are ignored              */
+    const float* bias_values;         /* [n_bias]                                                  */
+    int32_t n_bias;
+    const uint32_t* mask;             /* row (b, i) at mask + b*mask_stride_b + i*mask_stride_pos
+                                         (words): W words, bit v as in seen, 1 = token allowed     */
+    int64_t mask_stride_b, mask_stride_pos;
+} specv_adjustments;
+
+/* Penalties, biases and masks on logits rows.  Row (b, i) is position
+ * p = pos0 + i of the round.  With c(v) = counts[slot][v] plus the number of
+ * drafts d_j == v, j < p, and used(v) = seen bit or such a draft, the logit z
+ * of token v becomes, in float32 and this order,
+ *   used(v):        z > 0 ? z / repetition : z * repetition
+ *   c(v) > 0:       (z - frequency * c(v)) - presence
+ *   biased:         z + (the row's entries for v, added in list order)
+ *   mask bit 0:     -inf, whatever z was (NaN included)
+ * rounded once to dtype; logits that no step names keep their bits.  A row
+ * whose mask allows nothing is all -inf (verify calls flag it
+ * SPECV_FLAG_NONFINITE_ROW).
+ *   logits, out     [B, n_pos, V] of dtype; out may be logits itself: then
+ *                   only the 8-token groups that change are touched
+ *   pos0            position of the rows' first (0 for target rows; the
+ *                   drafter's position for its rows), 0 .. SPECV_MAX_GAMMA
+ * n_pos <= SPECV_MAX_GAMMA + 1.  B == 0 or n_pos == 0 is a no-op.  Errors:
+ * SPECV_E_NULL, SPECV_E_SHAPE, SPECV_E_DTYPE, SPECV_E_ALIGN,
+ * SPECV_E_CAPACITY, SPECV_E_HIP. */
+SPECV_API specv_status specv_adjust_logits(specv_handle h, void* stream,
+                                 const void* logits, int64_t stride_b, int64_t stride_pos,
+                                 void* out, int64_t out_stride_b, int64_t out_stride_pos,
+                                 specv_dtype dtype, int B, int n_pos, int V, int pos0,
+                                 const specv_adjustments* adj);
+
+/* Adds tokens to the histories of slots: for b in [0, B) and t in
+ * [0, lengths[b]), tokens[b][t] is marked in seen[slots[b]] and, unless
+ * ``prompt``, counted in counts[slots[b]].  With a verify call's out_tokens
+ * and num_emitted it takes a round's tokens in.  Entries outside [0, V) and
+ * slots outside [0, n_slots) are skipped; the same slot or token may come
+ * more than once.
+ *   slots           int32 [B]
+ *   tokens          int32 [B, n_tokens], token_stride entries per batch row
+ *   lengths         int32 [B] (cut to [0, n_tokens]), or NULL: n_tokens each
+ *   counts, seen    as in specv_adjustments
+ * Errors: SPECV_E_NULL, SPECV_E_SHAPE, SPECV_E_ALIGN, SPECV_E_CAPACITY,
+ * SPECV_E_HIP. */
+SPECV_API specv_status specv_history_add(specv_handle h, void* stream, const int32_t* slots,
+                                 const int32_t* tokens, int64_t token_stride, const int32_t* lengths,
+                                 int B, int n_tokens, int V, int prompt,
+                                 int32_t* counts, uint32_t* seen, int n_slots);
+
+/* Empties the histories of the listed slots (int32 [n]; others outside
+ * [0, n_slots) are skipped): the counts of their seen tokens and their seen
+ * words become 0.  Errors as specv_history_add. */
+SPECV_API specv_status specv_history_reset(specv_handle h, void* stream, const int32_t* slots, int n,
+                                 int V, int32_t* counts, uint32_t* seen, int n_slots);
+
+/* A teacher's record of logits rows: the K largest logits of each row (by
+ * value, descending; equal values by token, ascending) and two log-sum-exps
+ * at temperature T: of the whole row, log sum_v exp(z_v / T), and of the
+ * rest, the tokens outside the record (-inf when nothing finite is left).
+ *   logits          [B, n_pos, V] of dtype
+ *   K               1 .. SPECV_MAX_RECORD_K; entries behind the V-th are
+ *                   token -1, logit -inf
+ *   temperature     > 0, finite (SPECV_E_PARAM)
+ *   out_tokens      int32 [B, n_pos, K]
+ *   out_logits      float [B, n_pos, K], the raw logits
+ *   out_lse         float [B, n_pos, 2]: (whole row, rest), 8-byte aligned
+ * A row with NaN, +inf or no finite logit gets tokens -1, logits -inf and NaN
+ * log-sum-exps.  Errors: SPECV_E_NULL, SPECV_E_SHAPE, SPECV_E_DTYPE,
+ * SPECV_E_ALIGN, SPECV_E_CAPACITY, SPECV_E_PARAM, SPECV_E_HIP. */
+SPECV_API specv_status specv_top_logits(specv_handle h, void* stream,
+                                 const void* logits, int64_t stride_b, int64_t stride_pos,
+                                 specv_dtype dtype, int B, int n_pos, int V, int K, float temperature,
+                                 int32_t* out_tokens, float* out_logits, float* out_lse);
+
+/* A teacher's record (host struct of device pointers): entry (b, i) stands at
+ * b * stride_b + i of each array, as specv_top_logits writes them with
+ * stride_b = its n_pos (a larger stride_b leaves the rows behind the drafts,
+ * the bonus row, out).  Tokens outside [0, V) are ignored; the same token
+ * may come more than once (its probabilities add up). */
+typedef struct {
+    const int32_t* tokens;   /* [., K]                                                     */
+    const float* logits;     /* [., K]                                                     */
+    const float* lse;        /* [., 2], 8-byte aligned; may be NULL for SPECV_TAIL_RENORM   */
+    int64_t stride_b;        /* >= n_pos                                                   */
+    int32_t K;               /* 1 .. SPECV_MAX_RECORD_K                                    */
+} specv_teacher;
+
+/* What a record's missing tail counts for in the loss. */
+typedef enum {
+    SPECV_TAIL_RENORM = 0,   /* nothing: the teacher is the softmax over the record's logits */
+    SPECV_TAIL_BUCKET = 1    /* one more outcome, "any other token", of the probability that
+                                the record's log-sum-exps leave                            */
+} specv_tail;
+
+/* Distillation loss of student rows against a teacher's record at
+ * temperature T (the one the record was taken at).  With S the record's
+ * tokens, p_j the teacher's probabilities on them, q = softmax(z / T) over
+ * the student's whole row, and for SPECV_TAIL_BUCKET the rests
+ * p_o = exp(lse_rest - lse) and q_o = sum_{v not in S} q_v:
+ *   loss = w * (sum_j p_j (log p_j - log q_j) [ + p_o (log p_o - log q_o) ])
+ * terms with probability 0 left out.
+ *   student         [B, n_pos, V] of dtype
+ *   weights         float [B, n_pos] (w), or NULL: 1
+ *   out_loss        float [B, n_pos]; 0 where w == 0
+ *   out_lse         float [B, n_pos, 2]: the student's log-sum-exps of the whole
+ *                   row and of the tokens outside S, for specv_distill_grad;
+ *                   8-byte aligned
+ *   out_flags       int32 [B, n_pos] or NULL: SPECV_FLAG_NONFINITE_ROW or 0
+ * A record without a probability (NaN log-sum-exp, +inf or NaN logits, no
+ * token in [0, V) with a finite logit) leaves its row out: loss 0, flagged.
+ * A student row with NaN, +inf or no finite logit gives NaN, flagged; -inf
+ * logits are ordinary (a loss of +inf where the teacher has mass there).
+ * Errors: SPECV_E_NULL, SPECV_E_SHAPE, SPECV_E_DTYPE, SPECV_E_ALIGN,
+ * SPECV_E_CAPACITY, SPECV_E_PARAM (temperature, tail, K), SPECV_E_HIP. */
+SPECV_API specv_status specv_distill_loss(specv_handle h, void* stream,
+                                 const void* student, int64_t stride_b, int64_t stride_pos,
+                                 specv_dtype dtype, int B, int n_pos, int V,
+                                 const specv_teacher* teacher, const float* weights,
+                                 float temperature, specv_tail tail,
+                                 float* out_loss, float* out_lse, int32_t* out_flags);
+
+/* Its gradient: grad(b, i, v) = d loss / d z_v, rounded once to dtype:
+ *   w / T * (P q_v - p_v)                     v in S (p_v: its entries' sum)
+ *   w / T * (P q_v [ - p_o q_v / q_o ])       otherwise
+ * with P the sum of the teacher's probabilities.  ``student_lse`` is
+ * specv_distill_loss's out_lse on the same rows and record; put a gradient
+ * that reaches the loss into the weights.  Rows with w == 0 and rows whose
+ * record is left out get 0 and are not read; rows whose student_lse is NaN
+ * get NaN.  grad may be student itself.  Other arguments and errors as
+ * specv_distill_loss. */
+SPECV_API specv_status specv_distill_grad(specv_handle h, void* stream,
+                                 const void* student, int64_t stride_b, int64_t stride_pos,
+                                 specv_dtype dtype, int B, int n_pos, int V,
+                                 const specv_teacher* teacher, const float* weights,
+                                 float temperature, specv_tail tail, const float* student_lse,
+                                 void* grad, int64_t grad_stride_b, int64_t grad_stride_pos);
+
+/* Loss and gradient in one call, for weights known beforehand: the outputs of
+ * specv_distill_loss followed by specv_distill_grad, with the student's rows
+ * read once.  Rows with w == 0 are not read (loss 0, gradient 0, flag 0).
+ * grad may be student itself; out_flags may be NULL. */
+SPECV_API specv_status specv_distill_loss_grad(specv_handle h, void* stream,
+                                 const void* student, int64_t stride_b, int64_t stride_pos,
+                                 specv_dtype dtype, int B, int n_pos, int V,
+                                 const specv_teacher* teacher, const float* weights,
+                                 float temperature, specv_tail tail,
+                                 float* out_loss, int32_t* out_flags,
+                                 void* grad, int64_t grad_stride_b, int64_t grad_stride_pos);
 
 /* Kernel timing for measurement.  With enable != 0 every later call (verify
  * or sampler) records HIP events on its stream around its kernel (each call

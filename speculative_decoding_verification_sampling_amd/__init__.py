@@ -37,6 +37,11 @@ __all__ = [
     "read_ceiling",
     "verify_sample_noalloc",
     "debug_set_wait_limit",
+    "TokenHistory",
+    "make_penalties",
+    "make_bias",
+    "pack_token_mask",
+    "MAX_RECORD_K",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -57,7 +62,13 @@ EXPORTED_SYMBOLS = ("specv_create", "specv_verify_sample", "specv_verify_point_m
                     "specv_verify_sample_qstats", "specv_sample_draft", "specv_verify_greedy",
                     "specv_destroy", "specv_status_string", "specv_set_profiling",
                     "specv_get_profile", "specv_get_profile_samples", "specv_read_ceiling",
-                    "specv_verify_sample_noalloc", "specv_debug_set_wait_limit")
+                    "specv_verify_sample_noalloc", "specv_debug_set_wait_limit",
+                    "specv_adjust_logits", "specv_history_add", "specv_history_reset",
+                    "specv_top_logits", "specv_distill_loss", "specv_distill_grad",
+                    "specv_distill_loss_grad")
+
+MAX_RECORD_K = 256
+TAILS = {"renorm": 0, "bucket": 1}
 
 
 class SpecvError(RuntimeError):
@@ -73,6 +84,20 @@ class _Config(ctypes.Structure):
 class _Diag(ctypes.Structure):
     _fields_ = [("p_at_draft", ctypes.c_void_p), ("q_at_draft", ctypes.c_void_p),
                 ("residual_sum", ctypes.c_void_p)]
+
+
+class _Adjustments(ctypes.Structure):
+    _fields_ = [("penalties", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+                ("n_slots", ctypes.c_int32), ("draft_tokens", ctypes.c_void_p),
+                ("token_stride", ctypes.c_int64), ("bias_offsets", ctypes.c_void_p),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("n_bias", ctypes.c_int32), ("mask", ctypes.c_void_p),
+                ("mask_stride_b", ctypes.c_int64), ("mask_stride_pos", ctypes.c_int64)]
+
+
+class _Teacher(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("stride_b", ctypes.c_int64), ("K", ctypes.c_int32)]
 
 
 _lib = None
@@ -156,6 +181,20 @@ def load_library():
     lib.specv_read_ceiling.restype = ctypes.c_int
     lib.specv_verify_sample_noalloc.argtypes = [ctypes.c_int] + lib.specv_verify_sample.argtypes[1:]
     lib.specv_verify_sample_noalloc.restype = ctypes.c_int
+    c_int, f32 = ctypes.c_int, ctypes.c_float
+    rows = [vp, i64, i64, c_int, c_int, c_int, c_int]              # pointer, strides, dtype, B, n, V
+    teacher = [ctypes.POINTER(_Teacher), vp, f32, c_int]           # record, weights, temperature, tail
+    lib.specv_adjust_logits.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, c_int, c_int, c_int, c_int, c_int,
+                                        ctypes.POINTER(_Adjustments)]
+    lib.specv_history_add.argtypes = [vp, vp, vp, vp, i64, vp, c_int, c_int, c_int, c_int, vp, vp, c_int]
+    lib.specv_history_reset.argtypes = [vp, vp, vp, c_int, c_int, vp, vp, c_int]
+    lib.specv_top_logits.argtypes = [vp, vp, *rows, c_int, f32, vp, vp, vp]
+    lib.specv_distill_loss.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp]
+    lib.specv_distill_grad.argtypes = [vp, vp, *rows, *teacher, vp, vp, i64, i64]
+    lib.specv_distill_loss_grad.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp, i64, i64]
+    for name in ("adjust_logits", "history_add", "history_reset", "top_logits", "distill_loss", "distill_grad",
+                 "distill_loss_grad"):
+        getattr(lib, "specv_" + name).restype = c_int
     _lib = lib
     return lib
 
@@ -269,6 +308,64 @@ def debug_set_wait_limit(polls, device=None):
     fn.argtypes = [ctypes.c_int, ctypes.c_int32]
     fn.restype = ctypes.c_int
     _check(fn(dev, int(polls)), "specv_debug_set_wait_limit")
+
+
+class TokenHistory:
+    """Token histories of ``n_slots`` sequences for Verifier.adjust_logits:
+    ``counts`` int32 [n_slots, vocab] (occurrences among the generated tokens)
+    and ``seen`` int32 [n_slots, ceil(vocab / 32)] (bits: in the prompt or
+    generated).  Empty at first; Verifier.history_add and history_reset keep
+    them.  Existing tensors may be given instead."""
+
+    def __init__(self, n_slots, vocab, device="cuda", counts=None, seen=None):
+        self.n_slots, self.vocab = int(n_slots), int(vocab)
+        self.words = (self.vocab + 31) // 32
+        z = dict(dtype=torch.int32, device=device)
+        self.counts = torch.zeros(self.n_slots, self.vocab, **z) if counts is None else counts
+        self.seen = torch.zeros(self.n_slots, self.words, **z) if seen is None else seen
+        for t, n, cols in ((self.counts, "counts", self.vocab), (self.seen, "seen", self.words)):
+            if t.dtype != torch.int32 or not t.is_contiguous() or t.shape != (self.n_slots, cols):
+                raise SpecvError(f"{n} must be a contiguous int32 [{self.n_slots}, {cols}] tensor")
+        if self.counts.device != self.seen.device:
+            raise SpecvError("counts and seen must be on one device")
+
+
+def make_penalties(B, repetition=1.0, presence=0.0, frequency=0.0, slot=None, device="cuda"):
+    """specv_penalties[B] as an int32 tensor [B, 4] on ``device``.  Columns:
+    repetition, presence, frequency (float32 bits), slot.  Each argument is a
+    scalar or a length-B sequence; ``slot`` defaults to the row's number, and
+    -1 stands for an empty history.  repetition must be > 0."""
+    rec = np.zeros(B, dtype=[("r", "<f4"), ("a", "<f4"), ("f", "<f4"), ("s", "<i4")])
+    rec["r"] = repetition
+    rec["a"] = presence
+    rec["f"] = frequency
+    rec["s"] = np.arange(B) if slot is None else slot
+    if not (rec["r"] > 0).all():
+        raise SpecvError("repetition must be > 0 (1: off)")
+    return torch.from_numpy(rec.view(np.int32).reshape(B, 4).copy()).to(device)
+
+
+def make_bias(rows, device="cuda"):
+    """The (offsets, tokens, values) tensors of Verifier.adjust_logits from
+    one {token: bias} dict (or list of (token, bias) pairs, or None) per batch
+    row."""
+    pairs = [list(r.items()) if isinstance(r, dict) else list(r or ()) for r in rows]
+    offsets = np.zeros(len(pairs) + 1, np.int32)
+    offsets[1:] = np.cumsum([len(p) for p in pairs])
+    flat = [e for p in pairs for e in p]
+    tokens = np.array([t for t, _ in flat], np.int32)
+    values = np.array([x for _, x in flat], np.float32)
+    return tuple(torch.from_numpy(x).to(device) for x in (offsets, tokens, values))
+
+
+def pack_token_mask(allowed):
+    """Truth values [..., V] (True: token allowed) as the bit words int32
+    [..., ceil(V / 32)] of Verifier.adjust_logits, on the same device."""
+    V = allowed.shape[-1]
+    bits = torch.nn.functional.pad(allowed.to(torch.uint8), (0, -V % 32))
+    bits = bits.view(*allowed.shape[:-1], -1, 8)
+    weight = 1 << torch.arange(8, device=allowed.device, dtype=torch.uint8)
+    return (bits * weight).sum(-1, dtype=torch.uint8).view(torch.int32)
 
 
 class Verifier:
@@ -485,3 +582,203 @@ class Verifier:
             _ptr(o.get("row_flags")))
         _check(st, "specv_verify_greedy")
         return o
+
+    # ---- logits operators around a round
+
+    def _on_device(self, t, name, dtype=None):
+        if not t.is_cuda or t.device.index != self.device:
+            raise SpecvError(f"{name} must be on the handle's device (cuda:{self.device})")
+        if dtype is not None and t.dtype != dtype:
+            raise SpecvError(f"{name} must be {dtype}")
+
+    def _dense(self, t, name, dtype, shape):
+        self._on_device(t, name, dtype)
+        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise SpecvError(f"{name} must be a contiguous {dtype} {list(shape)} tensor, got {list(t.shape)}")
+
+    def _out_rows(self, t, name, like):
+        self._on_device(t, name, like.dtype)
+        if t.shape != like.shape:
+            raise SpecvError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        return _rows(t, name, None)
+
+    def adjust_logits(self, logits, penalties=None, history=None, draft_tokens=None, pos0=0, bias=None,
+                      mask=None, out=None):
+        """Penalties, biases and grammar masks on logits [B, n, V] (float32 or
+        bfloat16), the rows of positions pos0 .. pos0 + n - 1 of a round.
+
+        penalties     from make_penalties, with ``history`` (a TokenHistory;
+                      None: empty histories) and ``draft_tokens`` int32
+                      [B, >= pos0 + n - 1], which count as generated at the
+                      positions behind them (None: they do not)
+        bias          (offsets, tokens, values) from make_bias
+        mask          int32 bit words [B, n, ceil(V / 32)] from
+                      pack_token_mask (rows may be broadcast); bit 0: -inf
+        out           rows to write; ``logits`` itself: in place; None: new
+                      rows
+
+        Returns the written rows.  Asynchronous on the current stream."""
+        self._on_device(logits, "logits")
+        isb, isp = _rows(logits, "logits", None)
+        B, n, V = logits.shape
+        code = _dtype_code(logits)
+        if out is None:
+            out = torch.empty(B, n, V, dtype=logits.dtype, device=logits.device)
+        osb, osp = self._out_rows(out, "out", logits)
+        adj = _Adjustments()
+        if penalties is not None:
+            self._dense(penalties, "penalties", torch.int32, (B, 4))
+            adj.penalties = penalties.data_ptr()
+            if history is not None:
+                if history.vocab != V:
+                    raise SpecvError(f"history is of {history.vocab} tokens, the logits of {V}")
+                self._on_device(history.counts, "history")
+                adj.counts, adj.seen = history.counts.data_ptr(), history.seen.data_ptr()
+                adj.n_slots = history.n_slots
+            if draft_tokens is not None:
+                self._on_device(draft_tokens, "draft_tokens", torch.int32)
+                if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B or \
+                        draft_tokens.shape[1] < pos0 + n - 1 or not draft_tokens.is_contiguous():
+                    raise SpecvError("draft_tokens must be a contiguous int32 [B, >= pos0 + n - 1] tensor")
+                adj.draft_tokens, adj.token_stride = draft_tokens.data_ptr(), draft_tokens.shape[1]
+        elif history is not None or draft_tokens is not None:
+            raise SpecvError("history and draft_tokens need penalties")
+        if bias is not None:
+            offsets, tokens, values = bias
+            self._dense(offsets, "bias offsets", torch.int32, (B + 1,))
+            self._dense(tokens, "bias tokens", torch.int32, (tokens.numel(),))
+            self._dense(values, "bias values", torch.float32, (tokens.numel(),))
+            adj.bias_offsets, adj.bias_tokens = offsets.data_ptr(), tokens.data_ptr()
+            adj.bias_values, adj.n_bias = values.data_ptr(), tokens.numel()
+        if mask is not None:
+            self._on_device(mask, "mask", torch.int32)
+            if tuple(mask.shape) != (B, n, (V + 31) // 32) or (mask.shape[2] > 1 and mask.stride(2) != 1):
+                raise SpecvError("mask must be int32 [B, n, ceil(V / 32)], contiguous along the words")
+            adj.mask, adj.mask_stride_b, adj.mask_stride_pos = mask.data_ptr(), mask.stride(0), mask.stride(1)
+        st = load_library().specv_adjust_logits(self._h, self._stream(), _ptr(logits), isb, isp, _ptr(out), osb,
+                                                osp, code, B, n, V, int(pos0), ctypes.byref(adj))
+        _check(st, "specv_adjust_logits")
+        return out
+
+    def _history_args(self, history, slots):
+        self._on_device(history.counts, "history")
+        self._dense(slots, "slots", torch.int32, (slots.numel(),))
+        return _ptr(history.counts), _ptr(history.seen), history.n_slots
+
+    def history_add(self, history, slots, tokens, lengths=None, prompt=False):
+        """Adds tokens int32 [B, n] to the histories of ``slots`` int32 [B],
+        the first ``lengths`` int32 [B] of each row (None: all): as prompt
+        tokens (seen, not counted) or as generated ones.  Entries outside the
+        vocabulary are skipped, so a verify call's out_tokens can be given,
+        with or without its num_emitted.  In place, on the current stream."""
+        h = self._history_args(history, slots)
+        self._on_device(tokens, "tokens", torch.int32)
+        B = slots.numel()
+        if tokens.dim() != 2 or tokens.shape[0] != B or (tokens.shape[1] > 1 and tokens.stride(1) != 1):
+            raise SpecvError("tokens must be int32 [B, n], contiguous along n")
+        if lengths is not None:
+            self._dense(lengths, "lengths", torch.int32, (B,))
+        st = load_library().specv_history_add(
+            self._h, self._stream(), _ptr(slots), _ptr(tokens), tokens.stride(0), _ptr(lengths), B,
+            tokens.shape[1], history.vocab, int(bool(prompt)), *h)
+        _check(st, "specv_history_add")
+
+    def history_reset(self, history, slots):
+        """Empties the histories of ``slots`` (int32 [n]), on the current
+        stream."""
+        h = self._history_args(history, slots)
+        st = load_library().specv_history_reset(self._h, self._stream(), _ptr(slots), slots.numel(),
+                                                history.vocab, *h)
+        _check(st, "specv_history_reset")
+
+    def top_logits(self, logits, k, temperature=1.0):
+        """The teacher's record of logits [B, n, V]: {"tokens": int32
+        [B, n, k], "logits": float32 [B, n, k], "lse": float32 [B, n, 2]}, the
+        k <= 256 largest logits by value (equal ones by token) and the
+        log-sum-exps of logits / temperature over the row and over the tokens
+        outside the record.  Asynchronous on the current stream."""
+        self._on_device(logits, "logits")
+        sb, sp = _rows(logits, "logits", None)
+        B, n, V = logits.shape
+        k = int(k)
+        f = dict(dtype=torch.float32, device=logits.device)
+        out = {"tokens": torch.empty(B, n, max(k, 0), dtype=torch.int32, device=logits.device),
+               "logits": torch.empty(B, n, max(k, 0), **f), "lse": torch.empty(B, n, 2, **f)}
+        st = load_library().specv_top_logits(
+            self._h, self._stream(), _ptr(logits), sb, sp, _dtype_code(logits), B, n, V, k, float(temperature),
+            _ptr(out["tokens"]), _ptr(out["logits"]), _ptr(out["lse"]))
+        _check(st, "specv_top_logits")
+        return out
+
+    def _distill_args(self, student, record, weights, temperature, tail):
+        self._on_device(student, "student")
+        sb, sp = _rows(student, "student", None)
+        B, n, V = student.shape
+        if tail not in TAILS:
+            raise SpecvError(f"tail must be one of {sorted(TAILS)}")
+        tok, val, lse = record["tokens"], record["logits"], record.get("lse")
+        if tok.dim() != 3 or tok.shape[0] != B or tok.shape[1] < n:
+            raise SpecvError("the record's tokens must be int32 [B, >= n, K]")
+        m, K = tok.shape[1], tok.shape[2]
+        self._dense(tok, "record tokens", torch.int32, (B, m, K))
+        self._dense(val, "record logits", torch.float32, (B, m, K))
+        if lse is not None:
+            self._dense(lse, "record lse", torch.float32, (B, m, 2))
+        elif tail == "bucket":
+            raise SpecvError("tail='bucket' needs the record's lse")
+        if weights is not None:
+            self._dense(weights, "weights", torch.float32, (B, n))
+        rec = _Teacher(tok.data_ptr(), val.data_ptr(), lse.data_ptr() if lse is not None else None, m, K)
+        return (_ptr(student), sb, sp, _dtype_code(student), B, n, V, ctypes.byref(rec), _ptr(weights),
+                float(temperature), TAILS[tail])
+
+    def distill_loss(self, student, record, weights=None, temperature=1.0, tail="bucket"):
+        """Distillation loss of student logits [B, n, V] against a record of
+        top_logits (of n positions or more: those behind the n-th, such as the
+        bonus row, are left out), taken at ``temperature``.  ``weights``
+        float32 [B, n] scale the rows' losses (None: 1).  tail: "bucket" (the
+        tokens outside the record as one more outcome) or "renorm" (the
+        teacher renormalised over the record).  Returns {"loss": float32
+        [B, n], "lse": float32 [B, n, 2] (for distill_grad), "flags": int32
+        [B, n]}.  Asynchronous on the current stream."""
+        args = self._distill_args(student, record, weights, temperature, tail)
+        B, n = student.shape[:2]
+        f = dict(dtype=torch.float32, device=student.device)
+        out = {"loss": torch.empty(B, n, **f), "lse": torch.empty(B, n, 2, **f),
+               "flags": torch.empty(B, n, dtype=torch.int32, device=student.device)}
+        st = load_library().specv_distill_loss(self._h, self._stream(), *args, _ptr(out["loss"]),
+                                               _ptr(out["lse"]), _ptr(out["flags"]))
+        _check(st, "specv_distill_loss")
+        return out
+
+    def _grad_rows(self, student, grad):
+        if grad is None:
+            grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+        return (grad, *self._out_rows(grad, "grad", student))
+
+    def distill_grad(self, student, record, lse, weights=None, temperature=1.0, tail="bucket", grad=None):
+        """Gradient of distill_loss's weighted losses with respect to the
+        student's logits (in their dtype), from its ``lse``; ``grad`` may be
+        given, also as ``student`` itself.  A gradient that reaches the losses
+        goes into ``weights``.  Returns grad."""
+        args = self._distill_args(student, record, weights, temperature, tail)
+        self._dense(lse, "lse", torch.float32, (*student.shape[:2], 2))
+        grad, gsb, gsp = self._grad_rows(student, grad)
+        st = load_library().specv_distill_grad(self._h, self._stream(), *args, _ptr(lse), _ptr(grad), gsb, gsp)
+        _check(st, "specv_distill_grad")
+        return grad
+
+    def distill_loss_grad(self, student, record, weights=None, temperature=1.0, tail="bucket", grad=None):
+        """distill_loss and distill_grad in one call that reads the student's
+        rows once, for weights known beforehand.  Returns {"loss", "grad",
+        "flags"}; ``student.backward(out["grad"])`` takes the gradient on into
+        the student's model."""
+        args = self._distill_args(student, record, weights, temperature, tail)
+        B, n = student.shape[:2]
+        grad, gsb, gsp = self._grad_rows(student, grad)
+        out = {"loss": torch.empty(B, n, dtype=torch.float32, device=student.device), "grad": grad,
+               "flags": torch.empty(B, n, dtype=torch.int32, device=student.device)}
+        st = load_library().specv_distill_loss_grad(self._h, self._stream(), *args, _ptr(out["loss"]),
+                                                    _ptr(out["flags"]), _ptr(grad), gsb, gsp)
+        _check(st, "specv_distill_loss_grad")
+        return out

@@ -249,6 +249,22 @@ specv_status launch(specv_handle h, specv::Args& a, bool bf16, bool vec, void* s
 
 }  // namespace
 
+namespace specv {
+
+int handle_device(specv_handle h) { return h->cfg.device; }
+int handle_max_vocab(specv_handle h) { return h->cfg.max_vocab; }
+
+hipEvent_t* handle_events(specv_handle h, hipStream_t stream) {
+    if (!h->prof || capturing(stream)) return nullptr;
+    try {
+        return next_events(h);
+    } catch (...) {
+        return nullptr;
+    }
+}
+
+}  // namespace specv
+
 extern "C" {
 
 const char* specv_status_string(specv_status s) {

@@ -1,0 +1,191 @@
+"""Argument errors of the logits operators, on the CPU: they are returned
+before anything is enqueued, so a zeroed block that starts with the handle's
+configuration (its first member) stands for a handle, and no device is
+touched."""
+
+import ctypes
+
+import pytest
+import torch
+
+import speculative_decoding_verification_sampling_amd as sv
+
+NULL, SHAPE, DTYPE, ALIGN, CAPACITY, PARAM, OK = 1, 2, 3, 4, 5, 6, 0
+P = 1 << 20          # an address that is never read
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import os
+    if not os.path.exists(sv.library_path()):
+        from speculative_decoding_verification_sampling_amd import build
+        build.build()
+    return sv.load_library()
+
+
+@pytest.fixture(scope="module")
+def handle():
+    block = (ctypes.c_char * 65536)()
+    ctypes.memmove(block, ctypes.byref(sv._Config(0, 4, 5, 1000, 0)), ctypes.sizeof(sv._Config))
+    return block
+
+
+def _adj(**kw):
+    a = sv._Adjustments()
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+ADJ = dict(logits=P, sb=3000, sp=1000, out=P + (1 << 16), osb=3000, osp=1000, dtype=1, B=2, n=3, V=1000, pos0=0)
+
+
+def _adjust(lib, h, adj, **kw):
+    a = {**ADJ, **kw}
+    return lib.specv_adjust_logits(h, None, a["logits"], a["sb"], a["sp"], a["out"], a["osb"], a["osp"],
+                                   a["dtype"], a["B"], a["n"], a["V"], a["pos0"],
+                                   ctypes.byref(adj) if adj is not None else None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), DTYPE), (dict(B=-1), SHAPE), (dict(V=0), SHAPE), (dict(n=33), SHAPE), (dict(pos0=-1), SHAPE),
+    (dict(pos0=32), SHAPE), (dict(sb=-1), SHAPE), (dict(sp=1 << 50), SHAPE), (dict(osp=-1), SHAPE),
+    (dict(V=1001), CAPACITY), (dict(logits=None), NULL), (dict(out=None), NULL), (dict(logits=P + 1), ALIGN),
+    (dict(out=P + (1 << 16) + 1), ALIGN),
+    (dict(osp=999), SHAPE),                       # output rows overlap
+    (dict(osb=0), SHAPE),
+    (dict(out=P + 2), SHAPE),                     # output over the input, shifted
+    (dict(out=P, osb=4000), SHAPE),               # the same address, other strides
+    (dict(sb=0, out=P, osb=0), SHAPE),            # in place on broadcast rows
+    (dict(B=0), OK), (dict(n=0), OK),
+])
+def test_adjust_rows(lib, handle, kw, status):
+    assert _adjust(lib, handle, _adj(), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(penalties=P + 4), ALIGN), (dict(penalties=P, n_slots=-1), SHAPE), (dict(penalties=P, n_slots=1), NULL),
+    (dict(penalties=P, n_slots=1, counts=P, seen=P + 2), ALIGN),
+    (dict(penalties=P, draft_tokens=P, token_stride=1), SHAPE),
+    (dict(penalties=P, draft_tokens=P + 2, token_stride=2), ALIGN),
+    (dict(bias_offsets=P, n_bias=-1), SHAPE), (dict(bias_offsets=P, n_bias=1), NULL),
+    (dict(bias_offsets=P, n_bias=1, bias_tokens=P, bias_values=P + 2), ALIGN),
+    (dict(mask=P + 2), ALIGN), (dict(mask=P, mask_stride_b=-1), SHAPE),
+])
+def test_adjust_adjustments(lib, handle, kw, status):
+    assert _adjust(lib, handle, _adj(**kw)) == status
+    assert _adjust(lib, handle, None) == NULL
+    assert _adjust(lib, None, _adj()) == NULL
+
+
+def test_history(lib, handle):
+    def add(h=handle, slots=P, tokens=P, stride=5, lengths=None, B=2, n=5, V=1000, counts=P, seen=P, S=4):
+        return lib.specv_history_add(h, None, slots, tokens, stride, lengths, B, n, V, 0, counts, seen, S)
+    assert add(h=None) == NULL and add(slots=None) == NULL and add(tokens=None) == NULL
+    assert add(counts=None) == NULL and add(seen=None) == NULL
+    assert add(B=-1) == SHAPE and add(n=-1) == SHAPE and add(S=-1) == SHAPE and add(V=0) == SHAPE
+    assert add(stride=-1) == SHAPE and add(V=1001) == CAPACITY
+    assert add(tokens=P + 1) == ALIGN and add(lengths=P + 2) == ALIGN and add(seen=P + 2) == ALIGN
+    assert add(B=0) == OK and add(n=0) == OK and add(S=0) == OK
+
+    def reset(h=handle, slots=P, n=2, V=1000, counts=P, seen=P, S=4):
+        return lib.specv_history_reset(h, None, slots, n, V, counts, seen, S)
+    assert reset(h=None) == NULL and reset(slots=None) == NULL and reset(n=-1) == SHAPE
+    assert reset(V=1001) == CAPACITY and reset(counts=P + 2) == ALIGN and reset(n=0) == OK and reset(S=0) == OK
+
+
+def test_top_logits(lib, handle):
+    def top(h=handle, x=P, sb=3000, sp=1000, dtype=0, B=2, n=3, V=1000, K=4, T=1.0, tok=P, val=P, lse=P):
+        return lib.specv_top_logits(h, None, x, sb, sp, dtype, B, n, V, K, T, tok, val, lse)
+    assert top(h=None) == NULL and top(x=None) == NULL and top(tok=None) == NULL and top(lse=None) == NULL
+    for T in (0.0, -1.0, float("nan"), float("inf"), 1e-45):
+        assert top(T=T) == PARAM, T
+    assert top(K=0) == PARAM and top(K=257) == PARAM
+    assert top(dtype=3) == DTYPE and top(V=0) == SHAPE and top(sp=-1) == SHAPE and top(V=1001) == CAPACITY
+    assert top(B=1 << 20, n=1 << 20) == SHAPE
+    assert top(x=P + 2) == ALIGN and top(lse=P + 4) == ALIGN and top(val=P + 2) == ALIGN
+    assert top(B=0) == OK and top(n=0) == OK
+
+
+def test_distill(lib, handle):
+    def call(op, h=handle, x=P, sb=3000, sp=1000, dtype=0, B=2, n=3, V=1000, rec=True, tok=P, val=P, lse=P,
+             rsb=3, K=4, w=None, T=1.0, tail=1, loss=P, out=P, flags=None, g=P + (1 << 16), gsb=3000, gsp=1000):
+        r = sv._Teacher(tok, val, lse, rsb, K)
+        a = (h, None, x, sb, sp, dtype, B, n, V, ctypes.byref(r) if rec else None, w, T, tail)
+        if op == "loss":
+            return lib.specv_distill_loss(*a, loss, out, flags)
+        if op == "grad":
+            return lib.specv_distill_grad(*a, out, g, gsb, gsp)
+        return lib.specv_distill_loss_grad(*a, loss, flags, g, gsb, gsp)
+    for op in ("loss", "grad", "loss_grad"):
+        assert call(op, h=None) == NULL and call(op, x=None) == NULL and call(op, rec=False) == NULL
+        assert call(op, tok=None) == NULL and call(op, lse=None) == NULL
+        assert call(op, T=0.0) == PARAM and call(op, tail=2) == PARAM and call(op, K=0) == PARAM
+        assert call(op, K=257) == PARAM and call(op, rsb=2) == SHAPE and call(op, V=1001) == CAPACITY
+        assert call(op, dtype=7) == DTYPE and call(op, x=P + 2) == ALIGN and call(op, lse=P + 4) == ALIGN
+        assert call(op, w=P + 2) == ALIGN and call(op, B=0) == OK and call(op, n=0) == OK
+    for op in ("loss", "loss_grad"):
+        assert call(op, loss=None) == NULL and call(op, flags=P + 2) == ALIGN
+    assert call("loss", out=None) == NULL and call("grad", out=None) == NULL
+    assert call("loss", out=P + 4) == ALIGN and call("grad", out=P + 4) == ALIGN
+    for op in ("grad", "loss_grad"):
+        assert call(op, g=None) == NULL and call(op, gsp=-1) == SHAPE and call(op, gsp=10) == SHAPE
+        assert call(op, g=P + 2) == ALIGN and call(op, g=P + 4) == SHAPE
+        assert call(op, sb=0, sp=0, g=P, gsb=0, gsp=0) == SHAPE
+
+
+def test_struct_layouts_match_the_binding(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    fields = {"specv_adjustments": sv._Adjustments, "specv_teacher": sv._Teacher}
+    lines = []
+    for name, cls in fields.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f, _ in cls._fields_]
+    lines.append('printf("%zu\\n%zu\\n%d\\n", sizeof(specv_penalties), offsetof(specv_penalties, slot), '
+                 'SPECV_MAX_RECORD_K);')
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "specv.h"\nint main(void) {\n'
+                   + "\n".join(lines) + "\nreturn 0; }\n")
+    inc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    exe = tmp_path / "layout"
+    subprocess.run([gcc, "-std=c99", "-I", inc, str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for cls in fields.values():
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f).offset for f, _ in cls._fields_]
+    assert got == want + [16, 12, sv.MAX_RECORD_K]
+
+
+def test_host_helpers():
+    p = sv.make_penalties(2, [1.5, 1.0], 0.25, [0.5, 0.0], [3, -1], device="cpu")
+    assert p.view(torch.float32)[:, :3].tolist() == [[1.5, 0.25, 0.5], [1.0, 0.25, 0.0]]
+    assert p[:, 3].tolist() == [3, -1]
+    with pytest.raises(sv.SpecvError):
+        sv.make_penalties(1, 0.0, device="cpu")
+    off, tok, val = sv.make_bias([{5: 1.0}, None, [(2, 0.5), (2, -1.0)]], device="cpu")
+    assert off.tolist() == [0, 1, 1, 3] and tok.tolist() == [5, 2, 2] and val.tolist() == [1.0, 0.5, -1.0]
+    a = torch.zeros(2, 35, dtype=torch.bool)
+    a[0, 0] = a[0, 31] = a[0, 34] = True
+    w = sv.pack_token_mask(a)
+    assert w.dtype == torch.int32 and w.tolist() == [[-(1 << 31) + 1, 4], [0, 0]]
+    h = sv.TokenHistory(3, 70, device="cpu")
+    assert h.counts.shape == (3, 70) and h.seen.shape == (3, 3)
+    with pytest.raises(sv.SpecvError):
+        sv.TokenHistory(3, 70, counts=torch.zeros(3, 70), seen=h.seen)
+
+
+def test_binding_refuses_host_tensors():
+    v = sv.Verifier.__new__(sv.Verifier)
+    v._h, v.device = None, 0
+    x = torch.zeros(1, 1, 8)
+    for call in (lambda: v.adjust_logits(x), lambda: v.top_logits(x, 2),
+                 lambda: v.distill_loss(x, {"tokens": x, "logits": x, "lse": x}),
+                 lambda: v.history_reset(sv.TokenHistory(1, 8, device="cpu"), torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(sv.SpecvError):
+            call()
