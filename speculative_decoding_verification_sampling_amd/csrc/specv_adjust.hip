@@ -21,10 +21,6 @@ namespace {
 constexpr int kTok = 8;                        // tokens per thread: one byte of a bit row
 constexpr int kAdjChunk = kBlock * kTok;       // tokens per workgroup
 
-// 16 bytes at any element-aligned address.
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-
 // 8 logits as they are stored.
 template <bool BF16>
 struct Group;

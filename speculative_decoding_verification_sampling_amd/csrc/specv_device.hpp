@@ -139,6 +139,77 @@ __device__ inline void unpack16(const uint4& q, float* x) {
     }
 }
 
+// 16 bytes at any element-aligned address (one global_load / store_dwordx4:
+// gfx950 takes them unaligned).
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+
+// Group g (16 bytes: 8 bfloat16 or 4 float32 entries) of a row of V entries
+// at any address, entries past the end as -inf.  ``issue`` starts the load of
+// a whole group (others load group 0, or nothing when the row has none) and
+// ``finish`` puts the last, partial group and the ones past it right.
+template <bool BF16>
+struct RowGroup {
+    static constexpr int G = BF16 ? 8 : 4;
+    u32x4 q;
+    __device__ inline void issue(const void* row, long long g, int full) {
+        if (full > 0) q = static_cast<const u32x4_a2*>(row)[g < full ? g : 0];
+    }
+    __device__ inline void finish(const void* row, long long g, int full, int V) {
+        if (g < full) return;
+        const unsigned ninf = BF16 ? 0xFF80FF80u : 0xFF800000u;
+        unsigned w[4] = {ninf, ninf, ninf, ninf};
+        if (g == full) {
+            const int rem = V - full * G;
+#pragma unroll
+            for (int e = 0; e < G - 1; ++e) {
+                if (e < rem) {
+                    if constexpr (BF16) {
+                        const unsigned h = static_cast<const unsigned short*>(row)[(long long)full * G + e];
+                        w[e / 2] = (e & 1) ? ((w[e / 2] & 0xFFFFu) | (h << 16)) : ((w[e / 2] & 0xFFFF0000u) | h);
+                    } else {
+                        w[e] = static_cast<const unsigned*>(row)[(long long)full * G + e];
+                    }
+                }
+            }
+        }
+        q = u32x4{w[0], w[1], w[2], w[3]};
+    }
+    // A group that ``issue`` did not load becomes -inf.
+    __device__ inline void clear(long long g, int full) {
+        const unsigned ninf = BF16 ? 0xFF80FF80u : 0xFF800000u;
+        if (g >= full) q = u32x4{ninf, ninf, ninf, ninf};
+    }
+    __device__ inline float elem(int e) const {
+        if constexpr (BF16) return (e & 1) ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
+        else return __uint_as_float(q[e]);
+    }
+    // Keeps the group packed between two passes over it: the compiler would
+    // otherwise unpack it once and hold the floats, twice the registers.
+    __device__ inline void pin() { asm volatile("" : "+v"(q)); }
+    // G values rounded to the row's type (bfloat16: to nearest even).
+    __device__ inline void pack(const float (&x)[G]) {
+        if constexpr (BF16) {
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const bf16x2 h = {static_cast<__bf16>(x[2 * w]), static_cast<__bf16>(x[2 * w + 1])};
+                q[w] = __builtin_bit_cast(unsigned, h);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < G; ++e) q[e] = __float_as_uint(x[e]);
+        }
+    }
+    __device__ inline void store(void* row, long long g) const { static_cast<u32x4_a2*>(row)[g] = q; }
+};
+
+template <bool BF16>
+__device__ inline void store_elem(void* row, long long v, float x) {
+    if constexpr (BF16) static_cast<__bf16*>(row)[v] = static_cast<__bf16>(x);
+    else static_cast<float*>(row)[v] = x;
+}
+
 // Index (within the chunk) of entry k of this thread's x[]: 16-byte groups,
 // group g = j * kBlock + tid holds entries [g * G, g * G + G), so each load
 // instruction of the workgroup covers one contiguous 4 KB span.

@@ -6,10 +6,12 @@
 //   log q_v = x_v - L,  log q_o = L_o - L
 //   d loss / d z_v = w / T * (P q_v - p_v)                          v in S
 //                    w / T * (P exp(x_v - L) - p_o exp(x_v - L_o))  otherwise
-// One workgroup per row.  The tokens of S are marked in a bit row in LDS, so
-// that the sum over the rest is a sum of its own (as a difference of sums it
-// would lose what is left of a student that has learned S); S itself is
-// summed from its K gathered logits.
+//                  = c exp(x_v - L_o),  c = w / T * (P exp(L_o - L) - p_o)
+// so outside S a row takes one exponential per logit and one factor.  The
+// tokens of S are marked in a bit row in LDS, so that the sum over the rest
+// is a sum of its own (as a difference of sums it would lose what is left of
+// a student that has learned S); S itself is summed from its K gathered
+// logits, by one wave, which also takes the teacher's side.
 
 #include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
@@ -20,209 +22,468 @@
 namespace specv {
 namespace {
 
-constexpr int kDisBlock = 1024;
-constexpr int kDisWaves = kDisBlock / kWave;
 constexpr int kMaxK = SPECV_MAX_RECORD_K;
+constexpr int kE = kMaxK / kWave;                // record entries per lane of the wave that takes them
+constexpr int kMaxWaves = 16;
+constexpr int kLoads = 4;                        // groups a thread loads at once while streaming
 
 struct DistillScratch {
     int tok[kMaxK];              // the record's tokens; -1: ignored
-    float p[kMaxK];              // the teacher's probability (0 where ignored)
-    float red[kDisWaves], red2[kDisWaves];
+    float t[kMaxK];              // the teacher's logits / T
+    float p[kMaxK];              // the teacher's probabilities (0 where ignored)
+    float z[kMaxK];              // the student's logits
+    int rep[kMaxK];              // the entry stands for its token (others of the same do not)
+    float red[kMaxWaves], red2[kMaxWaves];
+    float P, p_rest;             // the teacher's sum and rest
+    float m_s, s_s;              // the student's maximum and sum over S
+    int ok, bad;                 // there is a probability; a logit of S is NaN or +inf
 };
-
-struct BlockMax {
-    __device__ static inline float wave(float x) { return wave_max(x); }
-    __device__ static inline float join(float a, float b) { return fmaxf(a, b); }
-};
-struct BlockSum {
-    __device__ static inline float wave(float x) { return wave_sum(x); }
-    __device__ static inline float join(float a, float b) { return a + b; }
-};
-template <typename Op>
-__device__ inline float block_reduce(float x, float* red) {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    x = Op::wave(x);
-    __syncthreads();
-    if (lane == 0) red[wave] = x;
-    __syncthreads();
-    x = red[0];
-    for (int w = 1; w < kDisWaves; ++w) x = Op::join(x, red[w]);
-    return x;
-}
 
 __device__ inline bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-template <bool BF16>
-__device__ inline void store_elem(void* row, long long v, float x) {
-    if constexpr (BF16) static_cast<__bf16*>(row)[v] = static_cast<__bf16>(x);
-    else static_cast<float*>(row)[v] = x;
+// (m, s) statistics joined across the wave.
+__device__ inline void wave_join_ms(float& m, float& s, float scale) {
+    const float M = wave_max(m);
+    s = wave_sum(m == -kInf ? 0.f : s * fast_exp2((m - M) * scale));
+    m = M;
 }
 
-// What a workgroup knows of its row's record: this thread's entry (threads
-// below K) and the sums over all.
-struct Record {
-    int tok;                     // -1: none
-    float p, logp;               // the entry's probability
-    float p_rest, logp_rest;     // the rest's (0 without a bucket)
-    float P;                     // sum of all of them
-    bool ok;                     // there is a probability
+// The record's entries, lane l of one wave taking l, l + 64, ..
+struct Entries {
+    int tok[kE];
+    float t[kE];
 };
 
-__device__ inline Record load_record(const DistillArgs& a, long long rec, DistillScratch& sc) {
-    const int tid = threadIdx.x;
-    Record r;
-    r.tok = -1;
-    float t = -kInf;
-    bool bad = false;
-    if (tid < a.K) {
-        const int v = a.tok[rec * a.K + tid];
-        if (v >= 0 && v < a.V) {
-            r.tok = v;
-            t = a.val[rec * a.K + tid] * a.inv_t;
-            bad = !(t <= 3.402823466e38f);
+__device__ inline void issue_entries(const DistillArgs& a, long long rec, Entries& r) {
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int u = 0; u < kE; ++u) {
+        r.tok[u] = -1;
+        r.t[u] = -kInf;
+        const int k = lane + u * kWave;
+        if (k < a.K) {
+            r.tok[u] = a.tok[rec * a.K + k];
+            r.t[u] = a.val[rec * a.K + k];
         }
     }
-    float lse = 0.f;
+}
+__device__ inline void finish_entries(const DistillArgs& a, Entries& r) {
+#pragma unroll
+    for (int u = 0; u < kE; ++u) {
+        if (r.tok[u] < 0 || r.tok[u] >= a.V) {
+            r.tok[u] = -1;
+            r.t[u] = -kInf;
+        }
+        r.t[u] *= a.inv_t;
+    }
+}
+
+// The teacher's side, in one wave: the probabilities of the entries (sc.p)
+// and of the rest.
+struct Teacher {
+    float P, p_rest, logp_rest;
+    bool ok;
+    float m, lse;                // log p_j = (t_j - m) - lse
+};
+
+__device__ inline Teacher take_teacher(const DistillArgs& a, long long rec, DistillScratch& sc) {
+    const int lane = threadIdx.x % kWave;
+    Teacher r;
+    bool bad = false;
+    float m = -kInf;
+    for (int k = lane; k < a.K; k += kWave) {
+        const float t = sc.t[k];
+        bad |= !(t <= 3.402823466e38f);
+        m = fmaxf(m, t);
+    }
+    r.lse = 0.f;
     r.p_rest = 0.f;
     r.logp_rest = -kInf;
     if (a.bucket) {
-        lse = a.tlse[rec * 2];
-        r.logp_rest = a.tlse[rec * 2 + 1] - lse;
+        r.m = a.tlse[rec * 2];
+        r.logp_rest = a.tlse[rec * 2 + 1] - r.m;
         r.p_rest = expf(r.logp_rest);
-        bad = bad || !finite(lse) || !finite(r.p_rest);
+        bad |= !finite(r.m) || !finite(r.p_rest);
     } else {
-        const float m = block_reduce<BlockMax>(t, sc.red);
-        const float e = t == -kInf ? 0.f : expf(t - m);
-        lse = m + logf(block_reduce<BlockSum>(e, sc.red2));
+        r.m = wave_max(m);
+        float e = 0.f;
+        for (int k = lane; k < a.K; k += kWave) e += sc.t[k] == -kInf ? 0.f : expf(sc.t[k] - r.m);
+        r.lse = logf(wave_sum(e));               // relative to m, as the logits
     }
-    r.logp = t - lse;
-    r.p = t == -kInf ? 0.f : expf(r.logp);
-    const float sum = block_reduce<BlockSum>(r.p, sc.red);
-    r.P = sum + r.p_rest;
-    r.ok = !__syncthreads_or(bad) && r.P > 0.f && finite(r.P);
-    if (tid < a.K) {
-        sc.tok[tid] = r.tok;
-        sc.p[tid] = r.p;
+    float sum = 0.f;
+    for (int k = lane; k < a.K; k += kWave) {
+        const float p = sc.t[k] == -kInf ? 0.f : expf((sc.t[k] - r.m) - r.lse);
+        sc.p[k] = p;
+        sum += p;
     }
-    __syncthreads();
+    r.P = wave_sum(sum) + r.p_rest;
+    r.ok = __ballot(bad) == 0 && r.P > 0.f && finite(r.P);
     return r;
 }
 
-// This thread's entry is the first of its token; ``p`` then gets the sum of
-// all its entries.
-__device__ inline bool first_entry(const DistillArgs& a, const Record& r, const DistillScratch& sc, float& p) {
-    if (r.tok < 0) return false;
-    p = 0.f;
-    bool first = true;
-    for (int k = 0; k < a.K; ++k)
-        if (sc.tok[k] == r.tok) {
-            if (k < (int)threadIdx.x) first = false;
-            p += sc.p[k];
-        }
-    return first;
+// The sum of the probabilities of all entries of token t.
+__device__ inline float token_p(const DistillArgs& a, const DistillScratch& sc, int t) {
+    float p = 0.f;
+    for (int k = 0; k < a.K; ++k) p += sc.tok[k] == t ? sc.p[k] : 0.f;
+    return p;
 }
 
-template <bool BF16, int OP>
-__global__ __launch_bounds__(kDisBlock) void k_distill(DistillArgs a) {
+// Statistics of G entries, those of S (bits of ``in``) left out.
+template <bool BF16>
+__device__ __forceinline__ void leave_out(RowGroup<BF16>& r, unsigned in) {
+    constexpr int G = RowGroup<BF16>::G;
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+        if (!((in >> e) & 1)) continue;
+        if constexpr (BF16) r.q[e / 2] = (e & 1) ? ((r.q[e / 2] & 0xFFFFu) | 0xFF800000u) : ((r.q[e / 2] & 0xFFFF0000u) | 0xFF80u);
+        else r.q[e] = 0xFF800000u;
+    }
+}
+
+// The bits of group g's tokens.
+template <bool BF16>
+__device__ inline unsigned group_bits(const unsigned* inside, int g) {
+    if constexpr (BF16) return reinterpret_cast<const unsigned char*>(inside)[g];
+    else return (reinterpret_cast<const unsigned char*>(inside)[g / 2] >> (4 * (g & 1))) & 0xF;
+}
+
+// One row by one workgroup of NT threads.  The first NG groups of a thread
+// stay in registers between the sums and the gradient; a longer row's others
+// are read again (the loss alone holds none).
+template <bool BF16, int NT, int NG, int OP>
+__global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
+    constexpr int G = RowGroup<BF16>::G, NW = NT / kWave;
     __shared__ DistillScratch sc;
     extern __shared__ unsigned inside[];          // one bit per token: in S
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int b = blockIdx.x / a.n, i = blockIdx.x % a.n;
     const void* row = row_ptr<BF16>(a.in, a.sb, a.sp, b, i);
     void* grow = OP == kDistillLoss ? nullptr : const_cast<void*>(row_ptr<BF16>(a.grad, a.g_sb, a.g_sp, b, i));
+    const long long rec = (long long)b * a.rec_sb + i;
     const float w = a.w ? a.w[blockIdx.x] : 1.f;
-    const Record r = load_record(a, (long long)b * a.rec_sb + i, sc);
+    const int full = a.V / G;
 
-    if (OP != kDistillLoss && (w == 0.f || !r.ok)) {
-        for (int v = tid; v < a.V; v += kDisBlock) store_elem<BF16>(grow, v, 0.f);
-        if (OP == kDistillLossGrad && tid == 0) {
+    if (OP == kDistillLossGrad && w == 0.f) {
+        RowGroup<BF16> zero;
+        zero.q = u32x4{0, 0, 0, 0};
+        for (int g = tid; g < full; g += NT) zero.store(grow, g);
+        for (int v = full * G + tid; v < a.V; v += NT) store_elem<BF16>(grow, v, 0.f);
+        if (tid == 0) {
             a.loss[blockIdx.x] = 0.f;
-            if (a.flags) a.flags[blockIdx.x] = w == 0.f ? 0 : SPECV_FLAG_NONFINITE_ROW;
+            if (a.flags) a.flags[blockIdx.x] = 0;
         }
         return;
     }
-    float p_tok = 0.f;
-    const bool first = first_entry(a, r, sc, p_tok);
-    const float z_tok = r.tok >= 0 ? load_elem<BF16>(row, r.tok) : -kInf;
 
-    float lse, lse_rest;
-    if (OP == kDistillGrad) {
-        lse = a.slse[(long long)blockIdx.x * 2];
-        lse_rest = a.slse[(long long)blockIdx.x * 2 + 1];
-    } else {
-        const int words = (a.V + 31) / 32;
-        for (int k = tid; k < words; k += kDisBlock) inside[k] = 0;
-        __syncthreads();
-        if (first) atomicOr(&inside[r.tok / 32], 1u << (r.tok % 32));
-        __syncthreads();
-        // the rest: running maximum and sum
-        float m = -kInf, s = 0.f;
-        unsigned bad = 0;
-        for (int v = tid; v < a.V; v += kDisBlock) {
-            const float x = load_elem<BF16>(row, v);
-            bad |= !(x <= 3.402823466e38f);
-            if ((inside[v / 32] >> (v % 32)) & 1) continue;
-            if (x > m) {
-                s *= fast_exp2((m - x) * a.scale);
-                m = x;
-            }
-            if (x > -kInf) s += fast_exp2((x - m) * a.scale);
-        }
-        const float M = block_reduce<BlockMax>(m, sc.red);
-        s = block_reduce<BlockSum>(m == -kInf ? 0.f : s * fast_exp2((m - M) * a.scale), sc.red2);
-        lse_rest = M == -kInf ? -kInf : fmaf(M, a.inv_t, logf(s));
-        // S
-        const float MS = block_reduce<BlockMax>(z_tok, sc.red);
-        const float MA = fmaxf(M, MS);
-        float sa = block_reduce<BlockSum>(first && z_tok > -kInf ? fast_exp2((z_tok - MA) * a.scale) : 0.f, sc.red2);
-        if (M > -kInf) sa += s * fast_exp2((M - MA) * a.scale);
-        lse = fmaf(MA, a.inv_t, logf(sa));
-        if (__syncthreads_or(bad) || MA == -kInf) lse = lse_rest = __builtin_nanf("");
-        const float term = r.p > 0.f ? r.p * (r.logp - (z_tok * a.inv_t - lse)) : 0.f;
-        float kl = block_reduce<BlockSum>(term, sc.red);
-        if (r.p_rest > 0.f) kl += r.p_rest * (r.logp_rest - (lse_rest - lse));
-        if (tid == 0) {
-            a.loss[blockIdx.x] = w == 0.f || !r.ok ? 0.f : w * kl;
-            if (OP == kDistillLoss) {
-                a.lse[(long long)blockIdx.x * 2] = lse;
-                a.lse[(long long)blockIdx.x * 2 + 1] = lse_rest;
-            }
-            if (a.flags) a.flags[blockIdx.x] = r.ok && lse == lse ? 0 : SPECV_FLAG_NONFINITE_ROW;
-        }
+    Entries r;
+    if (wave == 0) issue_entries(a, rec, r);
+    RowGroup<BF16> h[NG > 0 ? NG : 1];
+    if constexpr (NG > 0) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) h[j].issue(row, j * NT + tid, full);
     }
-    if (OP == kDistillLoss) return;
-
-    // gradient: the whole row by the rest's formula, then S over it
-    __syncthreads();                              // (in place) every logit of S has been read
-    const float g = w * a.inv_t;
-    for (int v = tid; v < a.V; v += kDisBlock) {
-        const float x = load_elem<BF16>(row, v) * a.inv_t;
-        float d = r.P * expf(x - lse);
-        if (r.p_rest > 0.f && lse_rest != -kInf) d -= r.p_rest * expf(x - lse_rest);
-        store_elem<BF16>(grow, v, g * d);
+    for (int k = tid; k < (a.V + 31) / 32; k += NT) inside[k] = 0;
+    __syncthreads();
+    if (wave == 0) {
+        finish_entries(a, r);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            const int k = lane + u * kWave;
+            if (k >= a.K) continue;
+            int rep = 0;
+            float z = -kInf;
+            if (r.tok[u] >= 0) {
+                const unsigned bit = 1u << (r.tok[u] % 32);
+                rep = !(atomicOr(&inside[r.tok[u] / 32], bit) & bit);
+                z = load_elem<BF16>(row, r.tok[u]);
+            }
+            sc.tok[k] = r.tok[u];
+            sc.t[k] = r.t[u];
+            sc.rep[k] = rep;
+            sc.z[k] = z;
+        }
     }
     __syncthreads();
-    if (first) store_elem<BF16>(grow, r.tok, g * (r.P * expf(z_tok * a.inv_t - lse) - p_tok));
+
+    // the rest's maximum and sum
+    float m = -kInf, s = 0.f;
+    if constexpr (NG > 0) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const int g = j * NT + tid;
+            if ((j + 1) * NT > full) h[j].clear(g, full);
+            const unsigned in = g < full ? group_bits<BF16>(inside, g) : 0;
+            if (__ballot(in != 0)) leave_out<BF16>(h[j], in);    // for good: S is written over the rest at the end
+#pragma unroll
+            for (int e = 0; e < G; ++e) m = fmaxf(m, h[j].elem(e));
+        }
+        const float ref = m == -kInf ? 0.f : m;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            h[j].pin();
+#pragma unroll
+            for (int e = 0; e < G; ++e) s += fast_exp2((h[j].elem(e) - ref) * a.scale);
+        }
+    }
+    if (NG * NT < full) {
+        RowGroup<BF16> nx[kLoads], x[kLoads];
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) nx[l].issue(row, (NG + l) * NT + tid, full);
+        for (int j = NG; j * NT < full; j += kLoads) {
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) x[l] = nx[l];
+            if ((j + kLoads) * NT < full) {
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l) nx[l].issue(row, (j + kLoads + l) * NT + tid, full);
+            }
+            float gm = -kInf, gs = 0.f;
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l) {
+                const int g = (j + l) * NT + tid;
+                x[l].clear(g, full);
+                const unsigned in = g < full ? group_bits<BF16>(inside, g) : 0;
+                if (__ballot(in != 0)) leave_out<BF16>(x[l], in);
+#pragma unroll
+                for (int e = 0; e < G; ++e) gm = fmaxf(gm, x[l].elem(e));
+            }
+            const float ref = gm == -kInf ? 0.f : gm;
+#pragma unroll
+            for (int l = 0; l < kLoads; ++l)
+#pragma unroll
+                for (int e = 0; e < G; ++e) gs += fast_exp2((x[l].elem(e) - ref) * a.scale);
+            merge_ms(m, s, gm, gs, a.scale);
+        }
+    }
+    bool bad = s != s;                             // NaN or +inf among them
+    if (tid == 0) {
+        for (int v = full * G; v < a.V; ++v) {     // the row's last, partial group
+            if ((inside[v / 32] >> (v % 32)) & 1) continue;
+            const float x = load_elem<BF16>(row, v);
+            bad |= !(x <= 3.402823466e38f);
+            merge_ms(m, s, x, x == -kInf ? 0.f : 1.f, a.scale);
+        }
+    }
+    if (bad) s = __builtin_nanf("");
+    wave_join_ms(m, s, a.scale);
+    if (__ballot(bad)) s = __builtin_nanf("");
+    if (lane == 0) {
+        sc.red[wave] = m;
+        sc.red2[wave] = s;
+    }
+    Teacher t{};
+    if (wave == 0) {
+        t = take_teacher(a, rec, sc);
+        float ms = -kInf, ss = 0.f;
+        bool bad_s = false;
+        for (int k = lane; k < a.K; k += kWave) {
+            ms = fmaxf(ms, sc.z[k]);
+            bad_s |= !(sc.z[k] <= 3.402823466e38f);
+        }
+        ms = wave_max(ms);
+        for (int k = lane; k < a.K; k += kWave)
+            if (sc.rep[k] && sc.z[k] > -kInf) ss += fast_exp2((sc.z[k] - ms) * a.scale);
+        ss = wave_sum(ss);
+        bad_s = __ballot(bad_s) != 0;
+        if (lane == 0) {
+            sc.P = t.P;
+            sc.p_rest = t.p_rest;
+            sc.m_s = ms;
+            sc.s_s = ss;
+            sc.ok = t.ok;
+            sc.bad = bad_s;
+        }
+    }
+    __syncthreads();
+    m = lane < NW ? sc.red[lane] : -kInf;
+    s = lane < NW ? sc.red2[lane] : 0.f;
+    bad = __ballot(s != s) != 0 || sc.bad;
+    wave_join_ms(m, s, a.scale);
+    const float m_all = fmaxf(m, sc.m_s);
+    bad |= m_all == -kInf;
+    float s_all = sc.s_s > 0.f ? sc.s_s * fast_exp2((sc.m_s - m_all) * a.scale) : 0.f;
+    const float share = m == -kInf ? 0.f : fast_exp2((m - m_all) * a.scale);
+    s_all += s * share;
+
+    if (OP != kDistillLoss) {
+        // the gradient: the whole row by the rest's formula, then S over it
+        float c = 0.f;
+        const float ref = m == -kInf ? 0.f : m;
+        const float gw = w * a.inv_t;
+        if (sc.ok) {
+            if (m > -kInf) c = gw * (sc.P * share / s_all - sc.p_rest / s);
+            if (bad) c = __builtin_nanf("");
+        }
+        if constexpr (NG > 0) {
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const int g = j * NT + tid;
+                h[j].pin();
+                float y[G];
+#pragma unroll
+                for (int e = 0; e < G; ++e) y[e] = fast_exp2((h[j].elem(e) - ref) * a.scale) * c;
+                if (!sc.ok)
+#pragma unroll
+                    for (int e = 0; e < G; ++e) y[e] = 0.f;
+                RowGroup<BF16> o;
+                o.pack(y);
+                if (g < full) o.store(grow, g);
+            }
+        }
+        for (int g = NG * NT + tid; g < full; g += NT) {
+            RowGroup<BF16> x;
+            x.issue(row, g, full);
+            float y[G];
+#pragma unroll
+            for (int e = 0; e < G; ++e) y[e] = sc.ok ? fast_exp2((x.elem(e) - ref) * a.scale) * c : 0.f;
+            x.pack(y);
+            x.store(grow, g);
+        }
+        if (tid == 0) {
+            for (int v = full * G; v < a.V; ++v) {
+                const float y = sc.ok ? fast_exp2((load_elem<BF16>(row, v) - ref) * a.scale) * c : 0.f;
+                store_elem<BF16>(grow, v, y);
+            }
+        }
+        __syncthreads();
+        if (wave == 0 && sc.ok) {
+            for (int k = lane; k < a.K; k += kWave) {
+                if (!sc.rep[k]) continue;
+                float y = gw * (sc.P * fast_exp2((sc.z[k] - m_all) * a.scale) / s_all - token_p(a, sc, sc.tok[k]));
+                if (bad) y = __builtin_nanf("");
+                store_elem<BF16>(grow, sc.tok[k], y);
+            }
+        }
+    }
+    if (wave == 0) {
+        const float log_all = logf(s_all);
+        float kl = 0.f;
+        for (int k = lane; k < a.K; k += kWave)
+            if (sc.p[k] > 0.f)
+                kl += sc.p[k] * (((sc.t[k] - t.m) - t.lse) - ((sc.z[k] - m_all) * a.inv_t - log_all));
+        kl = wave_sum(kl);
+        if (t.p_rest > 0.f) {
+            const float logq = m == -kInf ? -kInf : (m - m_all) * a.inv_t + (logf(s) - log_all);
+            kl += t.p_rest * (t.logp_rest - logq);
+        }
+        if (lane == 0) {
+            const float nan = __builtin_nanf("");
+            a.loss[blockIdx.x] = w == 0.f || !t.ok ? 0.f : bad ? nan : w * kl;
+            if (OP == kDistillLoss) {
+                a.lse[(long long)blockIdx.x * 2] = bad ? nan : fmaf(m_all, a.inv_t, log_all);
+                a.lse[(long long)blockIdx.x * 2 + 1] =
+                    bad ? nan : m == -kInf ? -kInf : fmaf(m, a.inv_t, logf(s));
+            }
+            if (a.flags) a.flags[blockIdx.x] = t.ok && !bad ? 0 : SPECV_FLAG_NONFINITE_ROW;
+        }
+    }
+}
+
+// The gradient from given log-sum-exps, a part of a row per workgroup.
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void k_distill_grad(DistillArgs a, int parts) {
+    constexpr int G = RowGroup<BF16>::G;
+    __shared__ DistillScratch sc;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const long long ri = blockIdx.x / parts;
+    const int part = blockIdx.x % parts;
+    const int b = (int)(ri / a.n), i = (int)(ri % a.n);
+    const void* row = row_ptr<BF16>(a.in, a.sb, a.sp, b, i);
+    void* grow = const_cast<void*>(row_ptr<BF16>(a.grad, a.g_sb, a.g_sp, b, i));
+    const float w = a.w ? a.w[ri] : 1.f;
+    const int full = a.V / G;
+    const int per = (full + parts - 1) / parts;    // groups of a part
+    const int g0 = min(part * per, full), g1 = min(g0 + per, full);
+    const int v0 = g0 * G, v1 = part == parts - 1 ? a.V : g1 * G;
+
+    const float lse = a.slse[ri * 2], lse_rest = a.slse[ri * 2 + 1];
+    if (wave == 0 && w != 0.f) {
+        const long long rec = (long long)b * a.rec_sb + i;
+        Entries r;
+        issue_entries(a, rec, r);
+        finish_entries(a, r);
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            const int k = lane + u * kWave;
+            if (k >= a.K) continue;
+            sc.tok[k] = r.tok[u];
+            sc.t[k] = r.t[u];
+            sc.z[k] = r.tok[u] >= v0 && r.tok[u] < v1 ? load_elem<BF16>(row, r.tok[u]) : 0.f;
+        }
+        const Teacher t = take_teacher(a, rec, sc);
+        if (lane == 0) {
+            sc.P = t.P;
+            sc.p_rest = t.p_rest;
+            sc.ok = t.ok;
+        }
+    }
+    __syncthreads();                                // (in place) this part's logits of S have been read
+    const bool on = w != 0.f && sc.ok;
+    const float gw = w * a.inv_t;
+    float c = 0.f, ref = 0.f;
+    if (on && lse_rest != -kInf) {
+        c = gw * (sc.P * expf(lse_rest - lse) - sc.p_rest);
+        ref = lse_rest / a.inv_t;
+    }
+    if (on && lse != lse) c = __builtin_nanf("");
+    for (int g = g0 + tid; g < g1; g += kBlock) {
+        RowGroup<BF16> x;
+        x.q = u32x4{0, 0, 0, 0};
+        if (on) {
+            x.issue(row, g, full);
+            float y[G];
+#pragma unroll
+            for (int e = 0; e < G; ++e) y[e] = fast_exp2((x.elem(e) - ref) * a.scale) * c;
+            x.pack(y);
+        }
+        x.store(grow, g);
+    }
+    for (int v = g1 * G + tid; v < v1; v += kBlock)
+        store_elem<BF16>(grow, v, on ? fast_exp2((load_elem<BF16>(row, v) - ref) * a.scale) * c : 0.f);
+    __syncthreads();
+    if (wave == 0 && on) {
+        for (int k = lane; k < a.K; k += kWave)
+            if (sc.tok[k] >= v0 && sc.tok[k] < v1)  // (entries of one token write the same)
+                store_elem<BF16>(grow, sc.tok[k],
+                                 gw * (sc.P * expf(sc.z[k] * a.inv_t - lse) - token_p(a, sc, sc.tok[k])));
+    }
+}
+
+template <typename... A>
+hipError_t launch(void (*fn)(A...), long long blocks, int threads, size_t lds, hipStream_t stream, hipEvent_t* ev,
+                  A... args) {
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (ev)
+        hipExtLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), lds, stream, ev[0], ev[1], 0, args...);
+    else
+        hipLaunchKernelGGL(fn, dim3((unsigned)blocks), dim3(threads), lds, stream, args...);
+    return hipGetLastError();
 }
 
 template <bool BF16>
-void (*pick(DistillOp op))(DistillArgs) {
-    if (op == kDistillLoss) return k_distill<BF16, kDistillLoss>;
-    if (op == kDistillGrad) return k_distill<BF16, kDistillGrad>;
-    return k_distill<BF16, kDistillLossGrad>;
+hipError_t launch_rows(const DistillArgs& a, DistillOp op, hipStream_t stream, hipEvent_t* ev) {
+    constexpr int G = RowGroup<BF16>::G;
+    const long long rows = (long long)a.B * a.n;
+    if (op == kDistillGrad) {
+        // parts of about 16 KB, fewer where there are rows enough to fill the device
+        const int full = a.V / G;
+        int parts = 1;
+        while (parts < 64 && rows * parts < 4096 && full / (parts * 2) >= kBlock) parts *= 2;
+        return launch(k_distill_grad<BF16>, rows * parts, kBlock, 0, stream, ev, a, parts);
+    }
+    const size_t lds = (size_t)((a.V + 31) / 32) * 4;    // at most 64 KB
+    if (op == kDistillLoss) return launch(k_distill<BF16, 512, 0, kDistillLoss>, rows, 512, lds, stream, ev, a);
+    const int per1024 = (a.V / G + 1023) / 1024;
+    if (a.V / G <= 256 * 8) return launch(k_distill<BF16, 256, 8, kDistillLossGrad>, rows, 256, lds, stream, ev, a);
+    if (per1024 <= 4) return launch(k_distill<BF16, 512, 8, kDistillLossGrad>, rows, 512, lds, stream, ev, a);
+    if (per1024 <= 8) return launch(k_distill<BF16, 1024, 8, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
+    if (per1024 <= 16) return launch(k_distill<BF16, 1024, 16, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
+    return launch(k_distill<BF16, 1024, 20, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
 }
 
 }  // namespace
 
 hipError_t launch_distill(const DistillArgs& a, DistillOp op, bool bf16, hipStream_t stream, hipEvent_t* ev) {
-    const long long rows = (long long)a.B * a.n;
-    auto fn = bf16 ? pick<true>(op) : pick<false>(op);
-    const size_t lds = op == kDistillGrad ? 0 : (size_t)((a.V + 31) / 32) * 4;    // at most 64 KB
-    if (ev)
-        hipExtLaunchKernelGGL(fn, dim3((unsigned)rows), dim3(kDisBlock), lds, stream, ev[0], ev[1], 0, a);
-    else
-        hipLaunchKernelGGL(fn, dim3((unsigned)rows), dim3(kDisBlock), lds, stream, a);
-    return hipGetLastError();
+    return bf16 ? launch_rows<true>(a, op, stream, ev) : launch_rows<false>(a, op, stream, ev);
 }
 
 }  // namespace specv

@@ -266,6 +266,7 @@ struct RecordArgs {
     int* tok;
     float* val;
     float* lse;
+    int blocks, reps;             // blocks per thread, loads of four groups per block (set by the launch)
 };
 hipError_t launch_top_logits(const RecordArgs& a, bool bf16, hipStream_t stream, hipEvent_t* ev);
 
