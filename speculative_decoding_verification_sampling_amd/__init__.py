@@ -102,6 +102,10 @@ class _Teacher(ctypes.Structure):
 
 _lib = None
 
+# The current stream's handle without a Stream object around it (a tenth of
+# the time), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 
 def library_path():
     return os.environ.get("SPECV_LIBRARY", os.path.join(_HERE, "libspecv.so"))
@@ -423,6 +427,8 @@ class Verifier:
         return np.frombuffer(buf, dtype=np.float32, count=n.value).copy()
 
     def _stream(self):
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(self.device))
         return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
 
     def _outputs(self, B, gamma, device, out):
@@ -586,21 +592,33 @@ class Verifier:
     # ---- logits operators around a round
 
     def _on_device(self, t, name, dtype=None):
-        if not t.is_cuda or t.device.index != self.device:
+        if t.get_device() != self.device:
             raise SpecvError(f"{name} must be on the handle's device (cuda:{self.device})")
-        if dtype is not None and t.dtype != dtype:
+        if dtype is not None and t.dtype is not dtype:
             raise SpecvError(f"{name} must be {dtype}")
 
     def _dense(self, t, name, dtype, shape):
-        self._on_device(t, name, dtype)
-        if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise SpecvError(f"{name} must be a contiguous {dtype} {list(shape)} tensor, got {list(t.shape)}")
+        if t.get_device() != self.device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            raise SpecvError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{self.device}, got "
+                             f"{t.dtype} {list(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _logits(self, t, name):
+        """(address, strides of the first two dimensions, dtype code, B, n, V) of logits rows."""
+        if t.get_device() != self.device:
+            raise SpecvError(f"{name} must be on the handle's device (cuda:{self.device})")
+        if t.dim() != 3:
+            raise SpecvError(f"{name} must be [B, positions, V], got {tuple(t.shape)}")
+        B, n, V = t.shape
+        sb, sp, sv = t.stride()
+        if sv != 1 and V > 1:
+            raise SpecvError(f"{name} must be contiguous along the vocabulary")
+        return t.data_ptr(), sb, sp, _dtype_code(t), B, n, V
 
     def _out_rows(self, t, name, like):
-        self._on_device(t, name, like.dtype)
-        if t.shape != like.shape:
-            raise SpecvError(f"{name} must have the shape {tuple(like.shape)}, got {tuple(t.shape)}")
-        return _rows(t, name, None)
+        if t.shape != like.shape or t.dtype is not like.dtype:
+            raise SpecvError(f"{name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+        return self._logits(t, name)[:3]
 
     def adjust_logits(self, logits, penalties=None, history=None, draft_tokens=None, pos0=0, bias=None,
                       mask=None, out=None):
@@ -618,17 +636,13 @@ class Verifier:
                       rows
 
         Returns the written rows.  Asynchronous on the current stream."""
-        self._on_device(logits, "logits")
-        isb, isp = _rows(logits, "logits", None)
-        B, n, V = logits.shape
-        code = _dtype_code(logits)
+        ptr, isb, isp, code, B, n, V = self._logits(logits, "logits")
         if out is None:
             out = torch.empty(B, n, V, dtype=logits.dtype, device=logits.device)
-        osb, osp = self._out_rows(out, "out", logits)
+        optr, osb, osp = self._out_rows(out, "out", logits)
         adj = _Adjustments()
         if penalties is not None:
-            self._dense(penalties, "penalties", torch.int32, (B, 4))
-            adj.penalties = penalties.data_ptr()
+            adj.penalties = self._dense(penalties, "penalties", torch.int32, (B, 4))
             if history is not None:
                 if history.vocab != V:
                     raise SpecvError(f"history is of {history.vocab} tokens, the logits of {V}")
@@ -636,34 +650,34 @@ class Verifier:
                 adj.counts, adj.seen = history.counts.data_ptr(), history.seen.data_ptr()
                 adj.n_slots = history.n_slots
             if draft_tokens is not None:
-                self._on_device(draft_tokens, "draft_tokens", torch.int32)
-                if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B or \
-                        draft_tokens.shape[1] < pos0 + n - 1 or not draft_tokens.is_contiguous():
+                if draft_tokens.dim() != 2 or draft_tokens.shape[1] < pos0 + n - 1:
                     raise SpecvError("draft_tokens must be a contiguous int32 [B, >= pos0 + n - 1] tensor")
-                adj.draft_tokens, adj.token_stride = draft_tokens.data_ptr(), draft_tokens.shape[1]
+                width = draft_tokens.shape[1]
+                adj.draft_tokens = self._dense(draft_tokens, "draft_tokens", torch.int32, (B, width))
+                adj.token_stride = width
         elif history is not None or draft_tokens is not None:
             raise SpecvError("history and draft_tokens need penalties")
         if bias is not None:
             offsets, tokens, values = bias
-            self._dense(offsets, "bias offsets", torch.int32, (B + 1,))
-            self._dense(tokens, "bias tokens", torch.int32, (tokens.numel(),))
-            self._dense(values, "bias values", torch.float32, (tokens.numel(),))
-            adj.bias_offsets, adj.bias_tokens = offsets.data_ptr(), tokens.data_ptr()
-            adj.bias_values, adj.n_bias = values.data_ptr(), tokens.numel()
+            n_bias = tokens.numel()
+            adj.bias_offsets = self._dense(offsets, "bias offsets", torch.int32, (B + 1,))
+            adj.bias_tokens = self._dense(tokens, "bias tokens", torch.int32, (n_bias,))
+            adj.bias_values = self._dense(values, "bias values", torch.float32, (n_bias,))
+            adj.n_bias = n_bias
         if mask is not None:
             self._on_device(mask, "mask", torch.int32)
-            if tuple(mask.shape) != (B, n, (V + 31) // 32) or (mask.shape[2] > 1 and mask.stride(2) != 1):
+            if mask.shape != (B, n, (V + 31) // 32) or (mask.shape[2] > 1 and mask.stride(2) != 1):
                 raise SpecvError("mask must be int32 [B, n, ceil(V / 32)], contiguous along the words")
             adj.mask, adj.mask_stride_b, adj.mask_stride_pos = mask.data_ptr(), mask.stride(0), mask.stride(1)
-        st = load_library().specv_adjust_logits(self._h, self._stream(), _ptr(logits), isb, isp, _ptr(out), osb,
-                                                osp, code, B, n, V, int(pos0), ctypes.byref(adj))
+        st = load_library().specv_adjust_logits(self._h, self._stream(), ptr, isb, isp, optr, osb, osp, code, B,
+                                                n, V, int(pos0), ctypes.byref(adj))
         _check(st, "specv_adjust_logits")
         return out
 
     def _history_args(self, history, slots):
         self._on_device(history.counts, "history")
-        self._dense(slots, "slots", torch.int32, (slots.numel(),))
-        return _ptr(history.counts), _ptr(history.seen), history.n_slots
+        return (self._dense(slots, "slots", torch.int32, (slots.numel(),)), history.counts.data_ptr(),
+                history.seen.data_ptr(), history.n_slots)
 
     def history_add(self, history, slots, tokens, lengths=None, prompt=False):
         """Adds tokens int32 [B, n] to the histories of ``slots`` int32 [B],
@@ -671,24 +685,22 @@ class Verifier:
         tokens (seen, not counted) or as generated ones.  Entries outside the
         vocabulary are skipped, so a verify call's out_tokens can be given,
         with or without its num_emitted.  In place, on the current stream."""
-        h = self._history_args(history, slots)
+        sptr, *h = self._history_args(history, slots)
         self._on_device(tokens, "tokens", torch.int32)
         B = slots.numel()
         if tokens.dim() != 2 or tokens.shape[0] != B or (tokens.shape[1] > 1 and tokens.stride(1) != 1):
             raise SpecvError("tokens must be int32 [B, n], contiguous along n")
-        if lengths is not None:
-            self._dense(lengths, "lengths", torch.int32, (B,))
+        lptr = None if lengths is None else self._dense(lengths, "lengths", torch.int32, (B,))
         st = load_library().specv_history_add(
-            self._h, self._stream(), _ptr(slots), _ptr(tokens), tokens.stride(0), _ptr(lengths), B,
-            tokens.shape[1], history.vocab, int(bool(prompt)), *h)
+            self._h, self._stream(), sptr, tokens.data_ptr(), tokens.stride(0), lptr, B, tokens.shape[1],
+            history.vocab, 1 if prompt else 0, *h)
         _check(st, "specv_history_add")
 
     def history_reset(self, history, slots):
         """Empties the histories of ``slots`` (int32 [n]), on the current
         stream."""
-        h = self._history_args(history, slots)
-        st = load_library().specv_history_reset(self._h, self._stream(), _ptr(slots), slots.numel(),
-                                                history.vocab, *h)
+        sptr, *h = self._history_args(history, slots)
+        st = load_library().specv_history_reset(self._h, self._stream(), sptr, slots.numel(), history.vocab, *h)
         _check(st, "specv_history_reset")
 
     def top_logits(self, logits, k, temperature=1.0):
@@ -697,40 +709,33 @@ class Verifier:
         k <= 256 largest logits by value (equal ones by token) and the
         log-sum-exps of logits / temperature over the row and over the tokens
         outside the record.  Asynchronous on the current stream."""
-        self._on_device(logits, "logits")
-        sb, sp = _rows(logits, "logits", None)
-        B, n, V = logits.shape
-        k = int(k)
-        f = dict(dtype=torch.float32, device=logits.device)
-        out = {"tokens": torch.empty(B, n, max(k, 0), dtype=torch.int32, device=logits.device),
-               "logits": torch.empty(B, n, max(k, 0), **f), "lse": torch.empty(B, n, 2, **f)}
-        st = load_library().specv_top_logits(
-            self._h, self._stream(), _ptr(logits), sb, sp, _dtype_code(logits), B, n, V, k, float(temperature),
-            _ptr(out["tokens"]), _ptr(out["logits"]), _ptr(out["lse"]))
+        rows = self._logits(logits, "logits")
+        B, n = rows[4:6]
+        k, dev = int(k), logits.device
+        tokens = torch.empty((B, n, max(k, 0)), dtype=torch.int32, device=dev)
+        values = torch.empty((B, n, max(k, 0)), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, n, 2), dtype=torch.float32, device=dev)
+        st = load_library().specv_top_logits(self._h, self._stream(), *rows, k, temperature, tokens.data_ptr(),
+                                             values.data_ptr(), lse.data_ptr())
         _check(st, "specv_top_logits")
-        return out
+        return {"tokens": tokens, "logits": values, "lse": lse}
 
     def _distill_args(self, student, record, weights, temperature, tail):
-        self._on_device(student, "student")
-        sb, sp = _rows(student, "student", None)
-        B, n, V = student.shape
+        rows = self._logits(student, "student")
+        B, n = rows[4:6]
         if tail not in TAILS:
             raise SpecvError(f"tail must be one of {sorted(TAILS)}")
-        tok, val, lse = record["tokens"], record["logits"], record.get("lse")
+        tok, lse = record["tokens"], record.get("lse")
         if tok.dim() != 3 or tok.shape[0] != B or tok.shape[1] < n:
             raise SpecvError("the record's tokens must be int32 [B, >= n, K]")
-        m, K = tok.shape[1], tok.shape[2]
-        self._dense(tok, "record tokens", torch.int32, (B, m, K))
-        self._dense(val, "record logits", torch.float32, (B, m, K))
-        if lse is not None:
-            self._dense(lse, "record lse", torch.float32, (B, m, 2))
-        elif tail == "bucket":
+        _, m, K = tok.shape
+        if lse is None and tail == "bucket":
             raise SpecvError("tail='bucket' needs the record's lse")
-        if weights is not None:
-            self._dense(weights, "weights", torch.float32, (B, n))
-        rec = _Teacher(tok.data_ptr(), val.data_ptr(), lse.data_ptr() if lse is not None else None, m, K)
-        return (_ptr(student), sb, sp, _dtype_code(student), B, n, V, ctypes.byref(rec), _ptr(weights),
-                float(temperature), TAILS[tail])
+        rec = _Teacher(self._dense(tok, "record tokens", torch.int32, (B, m, K)),
+                       self._dense(record["logits"], "record logits", torch.float32, (B, m, K)),
+                       None if lse is None else self._dense(lse, "record lse", torch.float32, (B, m, 2)), m, K)
+        wptr = None if weights is None else self._dense(weights, "weights", torch.float32, (B, n))
+        return (*rows, ctypes.byref(rec), wptr, temperature, TAILS[tail])
 
     def distill_loss(self, student, record, weights=None, temperature=1.0, tail="bucket"):
         """Distillation loss of student logits [B, n, V] against a record of
@@ -742,14 +747,14 @@ class Verifier:
         [B, n], "lse": float32 [B, n, 2] (for distill_grad), "flags": int32
         [B, n]}.  Asynchronous on the current stream."""
         args = self._distill_args(student, record, weights, temperature, tail)
-        B, n = student.shape[:2]
-        f = dict(dtype=torch.float32, device=student.device)
-        out = {"loss": torch.empty(B, n, **f), "lse": torch.empty(B, n, 2, **f),
-               "flags": torch.empty(B, n, dtype=torch.int32, device=student.device)}
-        st = load_library().specv_distill_loss(self._h, self._stream(), *args, _ptr(out["loss"]),
-                                               _ptr(out["lse"]), _ptr(out["flags"]))
+        B, n = args[4:6]
+        loss = torch.empty((B, n), dtype=torch.float32, device=student.device)
+        lse = torch.empty((B, n, 2), dtype=torch.float32, device=student.device)
+        flags = torch.empty((B, n), dtype=torch.int32, device=student.device)
+        st = load_library().specv_distill_loss(self._h, self._stream(), *args, loss.data_ptr(), lse.data_ptr(),
+                                               flags.data_ptr())
         _check(st, "specv_distill_loss")
-        return out
+        return {"loss": loss, "lse": lse, "flags": flags}
 
     def _grad_rows(self, student, grad):
         if grad is None:
@@ -762,9 +767,9 @@ class Verifier:
         given, also as ``student`` itself.  A gradient that reaches the losses
         goes into ``weights``.  Returns grad."""
         args = self._distill_args(student, record, weights, temperature, tail)
-        self._dense(lse, "lse", torch.float32, (*student.shape[:2], 2))
-        grad, gsb, gsp = self._grad_rows(student, grad)
-        st = load_library().specv_distill_grad(self._h, self._stream(), *args, _ptr(lse), _ptr(grad), gsb, gsp)
+        lptr = self._dense(lse, "lse", torch.float32, (*args[4:6], 2))
+        grad, gptr, gsb, gsp = self._grad_rows(student, grad)
+        st = load_library().specv_distill_grad(self._h, self._stream(), *args, lptr, gptr, gsb, gsp)
         _check(st, "specv_distill_grad")
         return grad
 
@@ -774,11 +779,11 @@ class Verifier:
         "flags"}; ``student.backward(out["grad"])`` takes the gradient on into
         the student's model."""
         args = self._distill_args(student, record, weights, temperature, tail)
-        B, n = student.shape[:2]
-        grad, gsb, gsp = self._grad_rows(student, grad)
-        out = {"loss": torch.empty(B, n, dtype=torch.float32, device=student.device), "grad": grad,
-               "flags": torch.empty(B, n, dtype=torch.int32, device=student.device)}
-        st = load_library().specv_distill_loss_grad(self._h, self._stream(), *args, _ptr(out["loss"]),
-                                                    _ptr(out["flags"]), _ptr(grad), gsb, gsp)
+        B, n = args[4:6]
+        grad, gptr, gsb, gsp = self._grad_rows(student, grad)
+        loss = torch.empty((B, n), dtype=torch.float32, device=student.device)
+        flags = torch.empty((B, n), dtype=torch.int32, device=student.device)
+        st = load_library().specv_distill_loss_grad(self._h, self._stream(), *args, loss.data_ptr(),
+                                                    flags.data_ptr(), gptr, gsb, gsp)
         _check(st, "specv_distill_loss_grad")
-        return out
+        return {"loss": loss, "grad": grad, "flags": flags}

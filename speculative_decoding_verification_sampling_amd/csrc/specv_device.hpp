@@ -204,6 +204,52 @@ struct RowGroup {
     __device__ inline void store(void* row, long long g) const { static_cast<u32x4_a2*>(row)[g] = q; }
 };
 
+// exp2((x - ref) * scale) for many x and one ref, as one fused multiply-add
+// each: 2^(x scale - R) with R = ref scale rounded, and the factor
+// ``fix`` = 2^(R - ref scale) that makes up for the rounding, applied to the
+// sum.  ``step`` where R overflows (ref near the type's lowest or largest
+// value): neighbouring floats are then far more than 128 apart in exponent,
+// and the exponential is 1 at ref and 0 below it.
+struct ExpRef {
+    float ref, nr, fix, scale;
+    bool step;
+    __device__ inline ExpRef(float r, float sc) : ref(r == -kInf ? 0.f : r), scale(sc) {
+        nr = -(ref * scale);
+        step = !(fabsf(nr) <= 3.402823466e38f);
+        fix = step ? 1.f : fast_exp2(-fmaf(ref, scale, nr));
+    }
+    __device__ inline float fast(float x) const { return fast_exp2(fmaf(x, scale, nr)); }
+    __device__ inline float at_step(float x) const {     // NaN for NaN and +inf, as ``fast``
+        return x < ref ? 0.f : x == ref && x <= 3.402823466e38f ? 1.f : __builtin_nanf("");
+    }
+    __device__ inline float any(float x) const { return step ? at_step(x) : fast(x) * fix; }
+};
+
+// Sum of exp2((x - ref) * scale) over N groups; ``ref`` is their maximum or
+// above it.
+template <int N, typename Group>
+__device__ __forceinline__ float sum_exp(Group (&r)[N], const ExpRef& x) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        r[j].pin();
+#pragma unroll
+        for (int e = 0; e < Group::G; ++e) s += x.fast(r[j].elem(e));
+    }
+    s *= x.fix;
+    if (__builtin_expect(__ballot(x.step) != 0, 0)) {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            r[j].pin();
+#pragma unroll
+            for (int e = 0; e < Group::G; ++e) t += x.at_step(r[j].elem(e));
+        }
+        s = x.step ? t : s;
+    }
+    return s;
+}
+
 template <bool BF16>
 __device__ inline void store_elem(void* row, long long v, float x) {
     if constexpr (BF16) static_cast<__bf16*>(row)[v] = static_cast<__bf16>(x);

@@ -25,7 +25,6 @@ namespace {
 constexpr int kMaxK = SPECV_MAX_RECORD_K;
 constexpr int kE = kMaxK / kWave;                // record entries per lane of the wave that takes them
 constexpr int kMaxWaves = 16;
-constexpr int kLoads = 4;                        // groups a thread loads at once while streaming
 
 struct DistillScratch {
     int tok[kMaxK];              // the record's tokens; -1: ignored
@@ -36,6 +35,7 @@ struct DistillScratch {
     float red[kMaxWaves], red2[kMaxWaves];
     float P, p_rest;             // the teacher's sum and rest
     float m_s, s_s;              // the student's maximum and sum over S
+    int twice;                   // a token comes more than once
     int ok, bad;                 // there is a probability; a logit of S is NaN or +inf
 };
 
@@ -140,6 +140,25 @@ __device__ __forceinline__ void leave_out(RowGroup<BF16>& r, unsigned in) {
     }
 }
 
+// A group's gradient outside S: c exp2((x - ref) scale), or 0 for a row left
+// out (whose logits may be anything).
+template <typename Group>
+__device__ __forceinline__ Group grad_group(Group& x, const ExpRef& er, float c, bool on) {
+    float y[Group::G];
+    const float cf = c * er.fix;
+    x.pin();
+#pragma unroll
+    for (int e = 0; e < Group::G; ++e) y[e] = er.fast(x.elem(e)) * cf;
+    if (__builtin_expect(er.step || !on, 0)) {
+        x.pin();
+#pragma unroll
+        for (int e = 0; e < Group::G; ++e) y[e] = on ? er.at_step(x.elem(e)) * c : 0.f;
+    }
+    Group o;
+    o.pack(y);
+    return o;
+}
+
 // The bits of group g's tokens.
 template <bool BF16>
 __device__ inline unsigned group_bits(const unsigned* inside, int g) {
@@ -150,8 +169,9 @@ __device__ inline unsigned group_bits(const unsigned* inside, int g) {
 // One row by one workgroup of NT threads.  The first NG groups of a thread
 // stay in registers between the sums and the gradient; a longer row's others
 // are read again (the loss alone holds none).
-template <bool BF16, int NT, int NG, int OP>
-__global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
+// Streamed groups are loaded LD at a time.
+template <bool BF16, int NT, int NG, int LD, int MW, int OP>
+__global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
     constexpr int G = RowGroup<BF16>::G, NW = NT / kWave;
     __shared__ DistillScratch sc;
     extern __shared__ unsigned inside[];          // one bit per token: in S
@@ -183,6 +203,7 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
         for (int j = 0; j < NG; ++j) h[j].issue(row, j * NT + tid, full);
     }
     for (int k = tid; k < (a.V + 31) / 32; k += NT) inside[k] = 0;
+    if (tid == 0) sc.twice = 0;
     __syncthreads();
     if (wave == 0) {
         finish_entries(a, r);
@@ -195,6 +216,7 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
             if (r.tok[u] >= 0) {
                 const unsigned bit = 1u << (r.tok[u] % 32);
                 rep = !(atomicOr(&inside[r.tok[u] / 32], bit) & bit);
+                if (!rep) sc.twice = 1;
                 z = load_elem<BF16>(row, r.tok[u]);
             }
             sc.tok[k] = r.tok[u];
@@ -217,28 +239,22 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
 #pragma unroll
             for (int e = 0; e < G; ++e) m = fmaxf(m, h[j].elem(e));
         }
-        const float ref = m == -kInf ? 0.f : m;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            h[j].pin();
-#pragma unroll
-            for (int e = 0; e < G; ++e) s += fast_exp2((h[j].elem(e) - ref) * a.scale);
-        }
+        s = sum_exp<NG>(h, ExpRef(m, a.scale));
     }
     if (NG * NT < full) {
-        RowGroup<BF16> nx[kLoads], x[kLoads];
+        RowGroup<BF16> nx[LD], x[LD];
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l) nx[l].issue(row, (NG + l) * NT + tid, full);
-        for (int j = NG; j * NT < full; j += kLoads) {
+        for (int l = 0; l < LD; ++l) nx[l].issue(row, (NG + l) * NT + tid, full);
+        for (int j = NG; j * NT < full; j += LD) {
 #pragma unroll
-            for (int l = 0; l < kLoads; ++l) x[l] = nx[l];
-            if ((j + kLoads) * NT < full) {
+            for (int l = 0; l < LD; ++l) x[l] = nx[l];
+            if ((j + LD) * NT < full) {
 #pragma unroll
-                for (int l = 0; l < kLoads; ++l) nx[l].issue(row, (j + kLoads + l) * NT + tid, full);
+                for (int l = 0; l < LD; ++l) nx[l].issue(row, (j + LD + l) * NT + tid, full);
             }
-            float gm = -kInf, gs = 0.f;
+            float gm = -kInf;
 #pragma unroll
-            for (int l = 0; l < kLoads; ++l) {
+            for (int l = 0; l < LD; ++l) {
                 const int g = (j + l) * NT + tid;
                 x[l].clear(g, full);
                 const unsigned in = g < full ? group_bits<BF16>(inside, g) : 0;
@@ -246,11 +262,7 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
 #pragma unroll
                 for (int e = 0; e < G; ++e) gm = fmaxf(gm, x[l].elem(e));
             }
-            const float ref = gm == -kInf ? 0.f : gm;
-#pragma unroll
-            for (int l = 0; l < kLoads; ++l)
-#pragma unroll
-                for (int e = 0; e < G; ++e) gs += fast_exp2((x[l].elem(e) - ref) * a.scale);
+            const float gs = sum_exp<LD>(x, ExpRef(gm, a.scale));
             merge_ms(m, s, gm, gs, a.scale);
         }
     }
@@ -307,7 +319,7 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
     if (OP != kDistillLoss) {
         // the gradient: the whole row by the rest's formula, then S over it
         float c = 0.f;
-        const float ref = m == -kInf ? 0.f : m;
+        const ExpRef er(m, a.scale);
         const float gw = w * a.inv_t;
         if (sc.ok) {
             if (m > -kInf) c = gw * (sc.P * share / s_all - sc.p_rest / s);
@@ -317,30 +329,18 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
                 const int g = j * NT + tid;
-                h[j].pin();
-                float y[G];
-#pragma unroll
-                for (int e = 0; e < G; ++e) y[e] = fast_exp2((h[j].elem(e) - ref) * a.scale) * c;
-                if (!sc.ok)
-#pragma unroll
-                    for (int e = 0; e < G; ++e) y[e] = 0.f;
-                RowGroup<BF16> o;
-                o.pack(y);
+                const RowGroup<BF16> o = grad_group(h[j], er, c, sc.ok != 0);
                 if (g < full) o.store(grow, g);
             }
         }
         for (int g = NG * NT + tid; g < full; g += NT) {
             RowGroup<BF16> x;
             x.issue(row, g, full);
-            float y[G];
-#pragma unroll
-            for (int e = 0; e < G; ++e) y[e] = sc.ok ? fast_exp2((x.elem(e) - ref) * a.scale) * c : 0.f;
-            x.pack(y);
-            x.store(grow, g);
+            grad_group(x, er, c, sc.ok != 0).store(grow, g);
         }
         if (tid == 0) {
             for (int v = full * G; v < a.V; ++v) {
-                const float y = sc.ok ? fast_exp2((load_elem<BF16>(row, v) - ref) * a.scale) * c : 0.f;
+                const float y = sc.ok ? er.any(load_elem<BF16>(row, v)) * c : 0.f;
                 store_elem<BF16>(grow, v, y);
             }
         }
@@ -348,7 +348,8 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
         if (wave == 0 && sc.ok) {
             for (int k = lane; k < a.K; k += kWave) {
                 if (!sc.rep[k]) continue;
-                float y = gw * (sc.P * fast_exp2((sc.z[k] - m_all) * a.scale) / s_all - token_p(a, sc, sc.tok[k]));
+                const float p = sc.twice ? token_p(a, sc, sc.tok[k]) : sc.p[k];
+                float y = gw * (sc.P * fast_exp2((sc.z[k] - m_all) * a.scale) / s_all - p);
                 if (bad) y = __builtin_nanf("");
                 store_elem<BF16>(grow, sc.tok[k], y);
             }
@@ -378,11 +379,17 @@ __global__ __launch_bounds__(NT) void k_distill(DistillArgs a) {
     }
 }
 
-// The gradient from given log-sum-exps, a part of a row per workgroup.
+// The gradient from given log-sum-exps: a part of a row, kGradLoads groups a
+// thread, per workgroup.  Its logits are on their way while one wave takes
+// the record; the tokens of S inside the part are written over it at the end.
+constexpr int kGradLoads = 4;
+
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void k_distill_grad(DistillArgs a, int parts) {
     constexpr int G = RowGroup<BF16>::G;
+    constexpr int kPart = kBlock * kGradLoads * G; // tokens of a part
     __shared__ DistillScratch sc;
+    __shared__ unsigned mark[kPart / 32];          // tokens of S seen so far
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const long long ri = blockIdx.x / parts;
     const int part = blockIdx.x % parts;
@@ -390,24 +397,35 @@ __global__ __launch_bounds__(kBlock) void k_distill_grad(DistillArgs a, int part
     const void* row = row_ptr<BF16>(a.in, a.sb, a.sp, b, i);
     void* grow = const_cast<void*>(row_ptr<BF16>(a.grad, a.g_sb, a.g_sp, b, i));
     const float w = a.w ? a.w[ri] : 1.f;
-    const int full = a.V / G;
-    const int per = (full + parts - 1) / parts;    // groups of a part
-    const int g0 = min(part * per, full), g1 = min(g0 + per, full);
-    const int v0 = g0 * G, v1 = part == parts - 1 ? a.V : g1 * G;
+    const int full = a.V / G, g0 = part * kBlock * kGradLoads;
+    const int v0 = part * kPart, v1 = min(v0 + kPart, a.V);
 
+    const long long rec = (long long)b * a.rec_sb + i;
     const float lse = a.slse[ri * 2], lse_rest = a.slse[ri * 2 + 1];
+    Entries r;
+    RowGroup<BF16> h[kGradLoads];
+    if (w != 0.f) {
+        if (wave == 0) issue_entries(a, rec, r);
+#pragma unroll
+        for (int l = 0; l < kGradLoads; ++l) h[l].issue(row, g0 + l * kBlock + tid, full);
+    }
+    for (int k = tid; k < kPart / 32; k += kBlock) mark[k] = 0;
+    if (tid == 0) sc.twice = 0;
+    __syncthreads();
     if (wave == 0 && w != 0.f) {
-        const long long rec = (long long)b * a.rec_sb + i;
-        Entries r;
-        issue_entries(a, rec, r);
         finish_entries(a, r);
 #pragma unroll
         for (int u = 0; u < kE; ++u) {
             const int k = lane + u * kWave;
             if (k >= a.K) continue;
-            sc.tok[k] = r.tok[u];
+            const int t = r.tok[u];
+            sc.tok[k] = t;
             sc.t[k] = r.t[u];
-            sc.z[k] = r.tok[u] >= v0 && r.tok[u] < v1 ? load_elem<BF16>(row, r.tok[u]) : 0.f;
+            if (t >= v0 && t < v1) {
+                const unsigned bit = 1u << (t % 32);
+                if (atomicOr(&mark[(t - v0) / 32], bit) & bit) sc.twice = 1;
+                sc.z[k] = load_elem<BF16>(row, t);
+            }
         }
         const Teacher t = take_teacher(a, rec, sc);
         if (lane == 0) {
@@ -425,26 +443,21 @@ __global__ __launch_bounds__(kBlock) void k_distill_grad(DistillArgs a, int part
         ref = lse_rest / a.inv_t;
     }
     if (on && lse != lse) c = __builtin_nanf("");
-    for (int g = g0 + tid; g < g1; g += kBlock) {
-        RowGroup<BF16> x;
-        x.q = u32x4{0, 0, 0, 0};
-        if (on) {
-            x.issue(row, g, full);
-            float y[G];
+    const ExpRef er(ref, a.scale);
 #pragma unroll
-            for (int e = 0; e < G; ++e) y[e] = fast_exp2((x.elem(e) - ref) * a.scale) * c;
-            x.pack(y);
-        }
-        x.store(grow, g);
+    for (int l = 0; l < kGradLoads; ++l) {
+        const int g = g0 + l * kBlock + tid;
+        if (g < full) grad_group(h[l], er, c, on).store(grow, g);
     }
-    for (int v = g1 * G + tid; v < v1; v += kBlock)
-        store_elem<BF16>(grow, v, on ? fast_exp2((load_elem<BF16>(row, v) - ref) * a.scale) * c : 0.f);
+    for (int v = max(full * G, v0) + tid; v < v1; v += kBlock)               // the row's last, partial group
+        store_elem<BF16>(grow, v, on ? er.any(load_elem<BF16>(row, v)) * c : 0.f);
     __syncthreads();
     if (wave == 0 && on) {
-        for (int k = lane; k < a.K; k += kWave)
-            if (sc.tok[k] >= v0 && sc.tok[k] < v1)  // (entries of one token write the same)
-                store_elem<BF16>(grow, sc.tok[k],
-                                 gw * (sc.P * expf(sc.z[k] * a.inv_t - lse) - token_p(a, sc, sc.tok[k])));
+        for (int k = lane; k < a.K; k += kWave) {
+            if (sc.tok[k] < v0 || sc.tok[k] >= v1) continue;
+            const float p = sc.twice ? token_p(a, sc, sc.tok[k]) : sc.p[k];     // (entries of one token write the same)
+            store_elem<BF16>(grow, sc.tok[k], gw * (sc.P * expf(sc.z[k] * a.inv_t - lse) - p));
+        }
     }
 }
 
@@ -464,20 +477,17 @@ hipError_t launch_rows(const DistillArgs& a, DistillOp op, hipStream_t stream, h
     constexpr int G = RowGroup<BF16>::G;
     const long long rows = (long long)a.B * a.n;
     if (op == kDistillGrad) {
-        // parts of about 16 KB, fewer where there are rows enough to fill the device
-        const int full = a.V / G;
-        int parts = 1;
-        while (parts < 64 && rows * parts < 4096 && full / (parts * 2) >= kBlock) parts *= 2;
+        const int per = kBlock * kGradLoads * G, parts = (a.V + per - 1) / per;
         return launch(k_distill_grad<BF16>, rows * parts, kBlock, 0, stream, ev, a, parts);
     }
     const size_t lds = (size_t)((a.V + 31) / 32) * 4;    // at most 64 KB
-    if (op == kDistillLoss) return launch(k_distill<BF16, 512, 0, kDistillLoss>, rows, 512, lds, stream, ev, a);
-    const int per1024 = (a.V / G + 1023) / 1024;
-    if (a.V / G <= 256 * 8) return launch(k_distill<BF16, 256, 8, kDistillLossGrad>, rows, 256, lds, stream, ev, a);
-    if (per1024 <= 4) return launch(k_distill<BF16, 512, 8, kDistillLossGrad>, rows, 512, lds, stream, ev, a);
-    if (per1024 <= 8) return launch(k_distill<BF16, 1024, 8, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
-    if (per1024 <= 16) return launch(k_distill<BF16, 1024, 16, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
-    return launch(k_distill<BF16, 1024, 20, kDistillLossGrad>, rows, 1024, lds, stream, ev, a);
+    if (op == kDistillLoss) return launch(k_distill<BF16, 512, 0, 4, 4, kDistillLoss>, rows, 512, lds, stream, ev, a);
+    const int full = a.V / G;
+#define SPECV_ROWS(NG, LD, MW) launch(k_distill<BF16, 1024, NG, LD, MW, kDistillLossGrad>, rows, 1024, lds, stream, ev, a)
+    if (full <= 4 * 1024) return SPECV_ROWS(4, 2, 8);
+    if constexpr (BF16) return SPECV_ROWS(6, 2, 8);
+    else return full <= 16 * 1024 ? SPECV_ROWS(16, 4, 4) : SPECV_ROWS(20, 4, 4);
+#undef SPECV_ROWS
 }
 
 }  // namespace
