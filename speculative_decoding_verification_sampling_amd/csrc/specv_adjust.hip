@@ -32,7 +32,7 @@ struct Group<true> {
         q = *reinterpret_cast<const u32x4_a2*>(static_cast<const unsigned short*>(row) + v);
     }
     __device__ inline void store(void* row, long long v) const {
-        *reinterpret_cast<u32x4_a2*>(static_cast<unsigned short*>(row) + v) = q;
+        __builtin_nontemporal_store(q, reinterpret_cast<u32x4_a2*>(static_cast<unsigned short*>(row) + v));
     }
     __device__ inline void load_part(const void* row, long long v, int m) {
         const unsigned short* p = static_cast<const unsigned short*>(row) + v;
@@ -72,8 +72,8 @@ struct Group<false> {
     }
     __device__ inline void store(void* row, long long v) const {
         float* p = static_cast<float*>(row) + v;
-        *reinterpret_cast<u32x4_a2*>(p) = q[0];
-        *reinterpret_cast<u32x4_a2*>(p + 4) = q[1];
+        __builtin_nontemporal_store(q[0], reinterpret_cast<u32x4_a2*>(p));
+        __builtin_nontemporal_store(q[1], reinterpret_cast<u32x4_a2*>(p + 4));
     }
     __device__ inline void load_part(const void* row, long long v, int m) {
         const unsigned* p = static_cast<const unsigned*>(row) + v;
@@ -97,68 +97,49 @@ struct Group<false> {
     }
 };
 
-struct BiasScratch {
-    float sum[kAdjChunk];        // the row's bias per token of the chunk
-    unsigned bits[kBlock / 4];   // one byte per thread: its tokens with a bias
-    int tok[kBlock];             // one batch of entries inside the chunk, in list order
-    float val[kBlock];
-    int wave_n[kWaves];
-};
-
-// The biases of batch row b inside the chunk at v0, added in list order:
-// entries are taken kBlock at a time and compacted in order; the first entry
-// of each token adds the later ones of its batch up.  Returns whether there
-// are any; sc.sum and sc.bits are then complete.  Whole workgroup.
-__device__ __forceinline__ bool gather_bias(const AdjustArgs& a, int b, int v0, int len, BiasScratch& sc) {
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+// The biases of batch row b on this thread's tokens v .. v + 7 (added in list
+// order into sum[]); returns their bits.  Every wave walks the row's entries
+// 64 at a time and stops only at those inside the chunk, so the workgroup
+// needs no LDS and no barrier for them.
+__device__ __forceinline__ unsigned gather_bias(const AdjustArgs& a, int b, int v0, int len, float (&sum)[kTok]) {
+    const int tid = threadIdx.x, lane = tid % kWave;
     const int lo = min(max(a.bias_off[b], 0), a.n_bias), hi = min(max(a.bias_off[b + 1], 0), a.n_bias);
-    if (lo >= hi) return false;
-    bool any = false;
-    for (int base = lo; base < hi; base += kBlock) {
-        const int i = min(base + tid, hi - 1);
-        const long long t = a.bias_tok[i];
+    unsigned bits = 0;
+    for (int base = lo; base < hi; base += kWave) {
+        const int i = min(base + lane, hi - 1);
+        const int t = a.bias_tok[i];
         const float val = a.bias_val[i];
-        const bool in = base + tid < hi && t >= v0 && t < (long long)v0 + len;
-        const unsigned long long m = __ballot(in);
-        if (lane == 0) sc.wave_n[wave] = __popcll(m);
-        __syncthreads();
-        int before = 0, total = 0;
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) before += sc.wave_n[w];
-            total += sc.wave_n[w];
-        }
-        if (total && !any) {
+        unsigned long long m = __ballot(base + lane < hi && t >= v0 && t - v0 < len);
+        while (m) {
+            const int k = __builtin_ctzll(m);
+            m &= m - 1;
+            const int rel = __builtin_amdgcn_readlane(t, k) - v0 - tid * kTok;
+            const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(val), k));
 #pragma unroll
-            for (int e = 0; e < kTok; ++e) sc.sum[tid + e * kBlock] = 0.f;
-            if (tid < kBlock / 4) sc.bits[tid] = 0;
-            any = true;
+            for (int e = 0; e < kTok; ++e)
+                if (rel == e) {
+                    sum[e] += x;
+                    bits |= 1u << e;
+                }
         }
-        const int my = before + __popcll(m & ((1ull << lane) - 1));
-        if (in) {
-            sc.tok[my] = (int)(t - v0);
-            sc.val[my] = val;
-        }
-        __syncthreads();
-        if (tid < total) {
-            const int rel = sc.tok[tid];
-            bool first = true;
-            for (int q = 0; q < tid; ++q) first = first && sc.tok[q] != rel;
-            if (first) {
-                float s = sc.sum[rel];
-                for (int q = tid; q < total; ++q)
-                    if (sc.tok[q] == rel) s += sc.val[q];
-                sc.sum[rel] = s;
-                atomicOr(&sc.bits[rel / 32], 1u << (rel % 32));
-            }
-        }
-        __syncthreads();
     }
-    return any;
+    return bits;
 }
 
-template <bool BF16>
-__global__ __launch_bounds__(kBlock) void k_adjust(AdjustArgs a) {
-    __shared__ BiasScratch sc;
+// x / d, correctly rounded, from inv = 1 / d correctly rounded: the quotient's
+// remainder corrects it once.  An infinite or NaN quotient stays.
+__device__ inline float divide(float x, float d, float inv) {
+    const float q = x * inv;
+    const float r = fmaf(-q, d, x);
+    return fabsf(q) <= 3.402823466e38f ? fmaf(r, inv, q) : q;
+}
+
+// kAhead positions are loaded at once (mask bytes first: a group of which the
+// mask leaves nothing is not read).  In place only the groups that change are
+// read and written.
+template <bool BF16, bool INPLACE>
+__global__ __launch_bounds__(kBlock, 8) void k_adjust(AdjustArgs a) {
+    constexpr int kAhead = 2;
     const int tid = threadIdx.x;
     const unsigned per_row = (unsigned)a.C * a.PG;
     const int b = blockIdx.x / per_row;
@@ -168,13 +149,39 @@ __global__ __launch_bounds__(kBlock) void k_adjust(AdjustArgs a) {
     const int len = min(kAdjChunk, a.V - v0);
     const int i0 = pg * a.pp, i1 = min(i0 + a.pp, a.n);
     const int m = min(max(len - tid * kTok, 0), kTok);        // this thread's tokens
+    const unsigned live = (1u << m) - 1;
     const long long v = (long long)v0 + tid * kTok;
+
+    Group<BF16> g[kAhead];
+    unsigned allowed[kAhead];
+    const auto load_masks = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            allowed[k] = live;
+            if (a.mask && i + k < i1 && m > 0)
+                allowed[k] &= reinterpret_cast<const unsigned char*>(a.mask + (long long)b * a.m_sb +
+                                                                     (long long)(i + k) * a.m_sp)[v / 8];
+        }
+    };
+    const auto load_rows = [&](int i, unsigned special) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const bool read = allowed[k] != 0 && (!INPLACE || (special & allowed[k]) || allowed[k] != live);
+            if (i + k < i1 && read) {
+                const void* in = row_ptr<BF16>(a.in, a.i_sb, a.i_sp, b, i + k);
+                if (m == kTok) g[k].load(in, v);
+                else g[k].load_part(in, v, m);
+            }
+        }
+    };
+    load_masks(i0);
+    if (!INPLACE) load_rows(i0, 0);                             // on their way during the preparations
 
     float rep = 1.f, pres = 0.f, freq = 0.f;
     unsigned used = 0;
-    int cnt[kTok];
+    float cnt[kTok], bias[kTok];
 #pragma unroll
-    for (int e = 0; e < kTok; ++e) cnt[e] = 0;
+    for (int e = 0; e < kTok; ++e) cnt[e] = bias[e] = 0.f;
     const int* tok = nullptr;
     if (a.pen) {
         const specv_penalties p = a.pen[b];
@@ -183,66 +190,74 @@ __global__ __launch_bounds__(kBlock) void k_adjust(AdjustArgs a) {
         freq = p.frequency;
         if (p.slot >= 0 && p.slot < a.n_slots && m > 0) {
             const long long words = (a.V + 31) / 32;
-            used = reinterpret_cast<const unsigned char*>(a.seen + p.slot * words)[v / 8];
-            used &= (1u << m) - 1;
+            used = reinterpret_cast<const unsigned char*>(a.seen + p.slot * words)[v / 8] & live;
             const int* cr = a.counts + (long long)p.slot * a.V + v;
+            if (used) {
 #pragma unroll
-            for (int e = 0; e < kTok; ++e)
-                if ((used >> e) & 1) cnt[e] = cr[e];
+                for (int e = 0; e < kTok; ++e)
+                    if ((used >> e) & 1) cnt[e] = (float)cr[e];
+            }
         }
         if (a.tokens) tok = a.tokens + (long long)b * a.tok_sb;
     }
-    unsigned biased = 0;
-    if (a.bias_off && gather_bias(a, b, v0, len, sc)) biased = (sc.bits[tid / 4] >> (8 * (tid % 4))) & 0xFF;
+    const unsigned biased = a.bias_off ? gather_bias(a, b, v0, len, bias) : 0;
+    const float inv = 1.f / rep;
 
-    const bool inplace = a.in == a.out;
     int p = 0;                                                  // drafts taken into the counts so far
-    for (int i = i0; i < i1; ++i) {
-        if (tok) {
-            for (const int before = a.pos0 + i; p < before; ++p) {
-                const long long t = tok[p];
-                if (t < v0 || t >= (long long)v0 + len) continue;   // uniform
-                const int rel = (int)(t - v0) - tid * kTok;
-#pragma unroll
-                for (int e = 0; e < kTok; ++e)
-                    if (rel == e) {
-                        cnt[e]++;
-                        used |= 1u << e;
-                    }
-            }
-        }
-        if (m == 0) continue;
-        unsigned allowed = 0xFF;
-        if (a.mask)
-            allowed = reinterpret_cast<const unsigned char*>(a.mask + (long long)b * a.m_sb +
-                                                             (long long)i * a.m_sp)[v / 8];
-        allowed |= 0xFFu << m;
-        const unsigned special = (used | biased) & allowed;
-        const bool masked = (allowed & ((1u << m) - 1)) != ((1u << m) - 1);
-        if (inplace && !special && !masked) continue;
-        const void* in = row_ptr<BF16>(a.in, a.i_sb, a.i_sp, b, i);
-        void* out = const_cast<void*>(row_ptr<BF16>(a.out, a.o_sb, a.o_sp, b, i));
-        Group<BF16> g{};
-        if ((allowed & ((1u << m) - 1)) != 0) {
-            if (m == kTok) g.load(in, v);
-            else g.load_part(in, v, m);
-        }
-        if (special) {
-#pragma unroll
-            for (int e = 0; e < kTok; ++e) {
-                if (!((special >> e) & 1)) continue;
-                float x = g.get(e);
-                if ((used >> e) & 1) {
-                    x = x > 0.f ? x / rep : x * rep;
-                    if (cnt[e] > 0) x = (x - freq * (float)cnt[e]) - pres;
+    for (int ib = i0; ib < i1; ib += kAhead) {
+        if (ib > i0) load_masks(ib);
+        if (INPLACE) {
+            // the drafts of these positions may still mark tokens
+            unsigned special = used | biased;
+            if (tok) {
+                for (int q = p; q < a.pos0 + min(ib + kAhead, i1) - 1; ++q) {
+                    const long long rel = (long long)tok[q] - v;
+                    if (rel >= 0 && rel < m) special |= 1u << rel;
                 }
-                if ((biased >> e) & 1) x += sc.sum[tid * kTok + e];
-                g.put(e, x);
             }
+            load_rows(ib, special);
+        } else if (ib > i0) {
+            load_rows(ib, 0);
         }
-        if (masked) g.mask(allowed);
-        if (m == kTok) g.store(out, v);
-        else g.store_part(out, v, m);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = ib + k;
+            if (i >= i1) break;
+            if (tok) {
+                for (const int before = a.pos0 + i; p < before; ++p) {
+                    const long long t = tok[p];
+                    if (t < v0 || t >= (long long)v0 + len) continue;   // uniform
+                    const int rel = (int)(t - v0) - tid * kTok;
+#pragma unroll
+                    for (int e = 0; e < kTok; ++e)
+                        if (rel == e) {
+                            cnt[e] += 1.f;
+                            used |= 1u << e;
+                        }
+                }
+            }
+            const unsigned special = (used | biased) & allowed[k];
+            if (m == 0 || (INPLACE && !special && allowed[k] == live)) continue;
+            if (special) {
+#pragma unroll
+                for (int e = 0; e < kTok; ++e) {
+                    if (!((special >> e) & 1)) continue;
+                    const float z = g[k].get(e);            // no branches in here: selects are cheaper
+                    const float q = divide(z, rep, inv);
+                    float x = z > 0.f ? q : z * rep;
+                    x = (used >> e) & 1 ? x : z;
+                    const float y = (x - freq * cnt[e]) - pres;
+                    x = cnt[e] > 0.f ? y : x;
+                    const float w = x + bias[e];
+                    x = (biased >> e) & 1 ? w : x;
+                    g[k].put(e, x);
+                }
+            }
+            if (allowed[k] != live) g[k].mask(allowed[k]);
+            void* out = const_cast<void*>(row_ptr<BF16>(a.out, a.o_sb, a.o_sp, b, i));
+            if (m == kTok) g[k].store(out, v);
+            else g[k].store_part(out, v, m);
+        }
     }
 }
 
@@ -300,7 +315,10 @@ hipError_t launch_adjust(AdjustArgs& a, bool bf16, hipStream_t stream, hipEvent_
     a.C = (a.V + kAdjChunk - 1) / kAdjChunk;
     a.pp = a.n;
     a.PG = (a.n + a.pp - 1) / a.pp;
-    return launch(bf16 ? k_adjust<true> : k_adjust<false>, (long long)a.B * a.PG * a.C, kBlock, stream, ev, a);
+    const bool inplace = a.in == a.out;
+    auto fn = bf16 ? (inplace ? k_adjust<true, true> : k_adjust<true, false>)
+                   : (inplace ? k_adjust<false, true> : k_adjust<false, false>);
+    return launch(fn, (long long)a.B * a.PG * a.C, kBlock, stream, ev, a);
 }
 
 hipError_t launch_history_add(const HistoryArgs& a, hipStream_t stream, hipEvent_t* ev) {

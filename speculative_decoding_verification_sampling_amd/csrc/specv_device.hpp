@@ -201,7 +201,11 @@ struct RowGroup {
             for (int e = 0; e < G; ++e) q[e] = __float_as_uint(x[e]);
         }
     }
-    __device__ inline void store(void* row, long long g) const { static_cast<u32x4_a2*>(row)[g] = q; }
+    // For rows that the device writes once and does not read again: past the
+    // caches, which keep what is read.
+    __device__ inline void store(void* row, long long g) const {
+        __builtin_nontemporal_store(q, static_cast<u32x4_a2*>(row) + g);
+    }
 };
 
 // exp2((x - ref) * scale) for many x and one ref, as one fused multiply-add
