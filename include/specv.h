@@ -455,6 +455,14 @@ typedef enum {
                                 the record's log-sum-exps leave                            */
 } specv_tail;
 
+/* Bytes of workspace (device memory, 16-byte aligned) with which
+ * specv_distill_loss and specv_distill_loss_grad take a call of these sizes
+ * in parts of rows, several workgroups a row, which is faster where the rows
+ * are few; 0 where it is not (and for sizes out of range).  The workspace is
+ * the call's until the stream has passed it: calls that may overlap, graphs
+ * that may be replayed at once included, need one each. */
+SPECV_API int64_t specv_distill_workspace(specv_dtype dtype, int B, int n_pos, int V, int K);
+
 /* Distillation loss of student rows against a teacher's record at
  * temperature T (the one the record was taken at).  With S the record's
  * tokens, p_j the teacher's probabilities on them, q = softmax(z / T) over
@@ -469,6 +477,8 @@ typedef enum {
  *                   row and of the tokens outside S, for specv_distill_grad;
  *                   8-byte aligned
  *   out_flags       int32 [B, n_pos] or NULL: SPECV_FLAG_NONFINITE_ROW or 0
+ *   workspace       workspace_bytes of device memory, at least
+ *                   specv_distill_workspace (SPECV_E_CAPACITY), or NULL
  * A record without a probability (NaN log-sum-exp, +inf or NaN logits, no
  * token in [0, V) with a finite logit) leaves its row out: loss 0, flagged.
  * A student row with NaN, +inf or no finite logit gives NaN, flagged; -inf
@@ -480,7 +490,8 @@ SPECV_API specv_status specv_distill_loss(specv_handle h, void* stream,
                                  specv_dtype dtype, int B, int n_pos, int V,
                                  const specv_teacher* teacher, const float* weights,
                                  float temperature, specv_tail tail,
-                                 float* out_loss, float* out_lse, int32_t* out_flags);
+                                 float* out_loss, float* out_lse, int32_t* out_flags,
+                                 void* workspace, int64_t workspace_bytes);
 
 /* Its gradient: grad(b, i, v) = d loss / d z_v, rounded once to dtype:
  *   w / T * (P q_v - p_v)                     v in S (p_v: its entries' sum)
@@ -498,9 +509,9 @@ SPECV_API specv_status specv_distill_grad(specv_handle h, void* stream,
                                  float temperature, specv_tail tail, const float* student_lse,
                                  void* grad, int64_t grad_stride_b, int64_t grad_stride_pos);
 
-/* Loss and gradient in one call, for weights known beforehand: the outputs of
- * specv_distill_loss followed by specv_distill_grad, with the student's rows
- * read once.  Rows with w == 0 are not read (loss 0, gradient 0, flag 0).
+/* Loss and gradient in one call, for weights known beforehand: what
+ * specv_distill_loss followed by specv_distill_grad gives (up to the order of
+ * the float32 sums), with the student's rows read about once.  Rows with w == 0 are not read (loss 0, gradient 0, flag 0).
  * grad may be student itself; out_flags may be NULL. */
 SPECV_API specv_status specv_distill_loss_grad(specv_handle h, void* stream,
                                  const void* student, int64_t stride_b, int64_t stride_pos,
@@ -508,7 +519,8 @@ SPECV_API specv_status specv_distill_loss_grad(specv_handle h, void* stream,
                                  const specv_teacher* teacher, const float* weights,
                                  float temperature, specv_tail tail,
                                  float* out_loss, int32_t* out_flags,
-                                 void* grad, int64_t grad_stride_b, int64_t grad_stride_pos);
+                                 void* grad, int64_t grad_stride_b, int64_t grad_stride_pos,
+                                 void* workspace, int64_t workspace_bytes);
 
 /* Kernel timing for measurement.  With enable != 0 every later call (verify
  * or sampler) records HIP events on its stream around its kernel (each call

@@ -65,7 +65,7 @@ EXPORTED_SYMBOLS = ("specv_create", "specv_verify_sample", "specv_verify_point_m
                     "specv_verify_sample_noalloc", "specv_debug_set_wait_limit",
                     "specv_adjust_logits", "specv_history_add", "specv_history_reset",
                     "specv_top_logits", "specv_distill_loss", "specv_distill_grad",
-                    "specv_distill_loss_grad")
+                    "specv_distill_loss_grad", "specv_distill_workspace")
 
 MAX_RECORD_K = 256
 TAILS = {"renorm": 0, "bucket": 1}
@@ -193,9 +193,11 @@ def load_library():
     lib.specv_history_add.argtypes = [vp, vp, vp, vp, i64, vp, c_int, c_int, c_int, c_int, vp, vp, c_int]
     lib.specv_history_reset.argtypes = [vp, vp, vp, c_int, c_int, vp, vp, c_int]
     lib.specv_top_logits.argtypes = [vp, vp, *rows, c_int, f32, vp, vp, vp]
-    lib.specv_distill_loss.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp]
+    lib.specv_distill_loss.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp, vp, i64]
     lib.specv_distill_grad.argtypes = [vp, vp, *rows, *teacher, vp, vp, i64, i64]
-    lib.specv_distill_loss_grad.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp, i64, i64]
+    lib.specv_distill_loss_grad.argtypes = [vp, vp, *rows, *teacher, vp, vp, vp, i64, i64, vp, i64]
+    lib.specv_distill_workspace.argtypes = [c_int] * 5
+    lib.specv_distill_workspace.restype = i64
     for name in ("adjust_logits", "history_add", "history_reset", "top_logits", "distill_loss", "distill_grad",
                  "distill_loss_grad"):
         getattr(lib, "specv_" + name).restype = c_int
@@ -737,6 +739,15 @@ class Verifier:
         wptr = None if weights is None else self._dense(weights, "weights", torch.float32, (B, n))
         return (*rows, ctypes.byref(rec), wptr, temperature, TAILS[tail])
 
+    def _distill_work(self, student, args, record):
+        """(address, bytes, tensor) of a call's own workspace, from torch's
+        allocator on the current stream; none where the library asks for none."""
+        n = load_library().specv_distill_workspace(*args[3:7], record["tokens"].shape[2])
+        if n == 0:
+            return None, 0, None
+        t = torch.empty(n, dtype=torch.uint8, device=student.device)
+        return t.data_ptr(), n, t
+
     def distill_loss(self, student, record, weights=None, temperature=1.0, tail="bucket"):
         """Distillation loss of student logits [B, n, V] against a record of
         top_logits (of n positions or more: those behind the n-th, such as the
@@ -751,8 +762,9 @@ class Verifier:
         loss = torch.empty((B, n), dtype=torch.float32, device=student.device)
         lse = torch.empty((B, n, 2), dtype=torch.float32, device=student.device)
         flags = torch.empty((B, n), dtype=torch.int32, device=student.device)
+        work = self._distill_work(student, args, record)
         st = load_library().specv_distill_loss(self._h, self._stream(), *args, loss.data_ptr(), lse.data_ptr(),
-                                               flags.data_ptr())
+                                               flags.data_ptr(), *work[:2])
         _check(st, "specv_distill_loss")
         return {"loss": loss, "lse": lse, "flags": flags}
 
@@ -783,7 +795,8 @@ class Verifier:
         grad, gptr, gsb, gsp = self._grad_rows(student, grad)
         loss = torch.empty((B, n), dtype=torch.float32, device=student.device)
         flags = torch.empty((B, n), dtype=torch.int32, device=student.device)
+        work = self._distill_work(student, args, record)
         st = load_library().specv_distill_loss_grad(self._h, self._stream(), *args, loss.data_ptr(),
-                                                    flags.data_ptr(), gptr, gsb, gsp)
+                                                    flags.data_ptr(), gptr, gsb, gsp, *work[:2])
         _check(st, "specv_distill_loss_grad")
         return {"loss": loss, "grad": grad, "flags": flags}

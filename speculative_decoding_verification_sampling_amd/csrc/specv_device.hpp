@@ -152,8 +152,13 @@ template <bool BF16>
 struct RowGroup {
     static constexpr int G = BF16 ? 8 : 4;
     u32x4 q;
+    // PAST: past the caches, for rows too many to be found there later.
+    template <bool PAST = false>
     __device__ inline void issue(const void* row, long long g, int full) {
-        if (full > 0) q = static_cast<const u32x4_a2*>(row)[g < full ? g : 0];
+        if (full <= 0) return;
+        const u32x4_a2* p = static_cast<const u32x4_a2*>(row) + (g < full ? g : 0);
+        if constexpr (PAST) q = __builtin_nontemporal_load(p);
+        else q = *p;
     }
     __device__ inline void finish(const void* row, long long g, int full, int V) {
         if (g < full) return;

@@ -284,12 +284,19 @@ struct DistillArgs {
     float scale, inv_t;           // log2(e) / T, 1 / T
     int bucket;
     const float* slse;            // the student's log-sum-exps (gradient alone)
+    float2* part;                 // workspace (nullptr: none): [row][parts] (max, sum) of the rest
+    float* zs;                    // [row][2][K]: the student's logits of S; 1 where an entry stands for
+                                  // its token
+    int parts;
     float* loss;
     float* lse;
     int* flags;
     void* grad;
     long long g_sb, g_sp;
 };
+// Bytes of workspace that make the rows' parts separate workgroups; 0 where
+// one workgroup per row is as fast.
+size_t distill_workspace(DistillOp op, bool bf16, long long rows, int V, int K);
 hipError_t launch_distill(const DistillArgs& a, DistillOp op, bool bf16, hipStream_t stream, hipEvent_t* ev);
 
 }  // namespace specv

@@ -123,6 +123,20 @@ specv_status grad_args(const specv::DistillArgs& a, specv_dtype dtype, void* gra
     return SPECV_OK;
 }
 
+// Takes a given workspace, when it is large enough and parts are worth it.
+specv_status use_workspace(specv::DistillArgs& a, specv::DistillOp op, specv_dtype dtype, void* workspace,
+                           int64_t bytes) {
+    if (!workspace) return SPECV_OK;
+    if (!aligned(workspace, 16)) return SPECV_E_ALIGN;
+    const size_t need = specv::distill_workspace(op, dtype == SPECV_BF16, (long long)a.B * a.n, a.V, a.K);
+    if (bytes < 0 || (size_t)bytes < need) return SPECV_E_CAPACITY;
+    if (need == 0) return SPECV_OK;
+    const size_t z = (size_t)a.B * a.n * 2 * a.K * sizeof(float);
+    a.part = static_cast<float2*>(workspace);
+    a.zs = reinterpret_cast<float*>(static_cast<char*>(workspace) + (need - z));
+    return SPECV_OK;
+}
+
 specv_status launch_distill_op(specv_handle h, void* stream, const specv::DistillArgs& a, specv::DistillOp op,
                                specv_dtype dtype) {
     DeviceScope dev(specv::handle_device(h));
@@ -284,12 +298,20 @@ specv_status specv_top_logits(specv_handle h, void* stream, const void* logits, 
     return done(specv::launch_top_logits(a, dtype == SPECV_BF16, s, specv::handle_events(h, s)));
 }
 
+int64_t specv_distill_workspace(specv_dtype dtype, int B, int n_pos, int V, int K) {
+    if ((dtype != SPECV_F32 && dtype != SPECV_BF16) || B < 0 || n_pos < 0 || V < 1 || V > SPECV_MAX_VOCAB || K < 1 ||
+        K > SPECV_MAX_RECORD_K)
+        return 0;
+    return (int64_t)specv::distill_workspace(specv::kDistillLossGrad, dtype == SPECV_BF16, (long long)B * n_pos, V, K);
+}
+
 specv_status specv_distill_loss(specv_handle h, void* stream, const void* student, int64_t stride_b,
                                 int64_t stride_pos, specv_dtype dtype, int B, int n_pos, int V,
                                 const specv_teacher* teacher, const float* weights, float temperature,
-                                specv_tail tail, float* out_loss, float* out_lse, int32_t* out_flags) {
+                                specv_tail tail, float* out_loss, float* out_lse, int32_t* out_flags,
+                                void* workspace, int64_t workspace_bytes) {
     specv::DistillArgs a{};
-    const specv_status st = distill_args(h, student, stride_b, stride_pos, dtype, B, n_pos, V, teacher, weights,
+    specv_status st = distill_args(h, student, stride_b, stride_pos, dtype, B, n_pos, V, teacher, weights,
                                          temperature, tail, &a);
     if (st != SPECV_OK || B == 0 || n_pos == 0) return st;
     if (!out_loss || !out_lse) return SPECV_E_NULL;
@@ -297,6 +319,8 @@ specv_status specv_distill_loss(specv_handle h, void* stream, const void* studen
     a.loss = out_loss;
     a.lse = out_lse;
     a.flags = out_flags;
+    st = use_workspace(a, specv::kDistillLoss, dtype, workspace, workspace_bytes);
+    if (st != SPECV_OK) return st;
     return launch_distill_op(h, stream, a, specv::kDistillLoss, dtype);
 }
 
@@ -324,7 +348,8 @@ specv_status specv_distill_loss_grad(specv_handle h, void* stream, const void* s
                                      int64_t stride_pos, specv_dtype dtype, int B, int n_pos, int V,
                                      const specv_teacher* teacher, const float* weights, float temperature,
                                      specv_tail tail, float* out_loss, int32_t* out_flags, void* grad,
-                                     int64_t grad_stride_b, int64_t grad_stride_pos) {
+                                     int64_t grad_stride_b, int64_t grad_stride_pos, void* workspace,
+                                     int64_t workspace_bytes) {
     specv::DistillArgs a{};
     specv_status st = distill_args(h, student, stride_b, stride_pos, dtype, B, n_pos, V, teacher, weights,
                                    temperature, tail, &a);
@@ -338,6 +363,8 @@ specv_status specv_distill_loss_grad(specv_handle h, void* stream, const void* s
     a.grad = grad;
     a.g_sb = grad_stride_b;
     a.g_sp = grad_stride_pos;
+    st = use_workspace(a, specv::kDistillLossGrad, dtype, workspace, workspace_bytes);
+    if (st != SPECV_OK) return st;
     return launch_distill_op(h, stream, a, specv::kDistillLossGrad, dtype);
 }
 

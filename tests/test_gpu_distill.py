@@ -129,12 +129,28 @@ def _check(student, rec, weights, T, tail, out, grad, skip_zero=False):
                        None if g is None else g[b, i], None if flags is None else int(flags[b, i]), skip_zero)
 
 
+def _no_workspace(v):
+    """The calls of v then take one workgroup per row."""
+    v._distill_work = lambda *a: (None, 0, None)
+
+
 def _run(student, rec, weights, T, tail):
-    """The three calls on the same rows; all outputs checked."""
+    """The three calls on the same rows; all outputs checked, with and without
+    a workspace (parts of rows, whole rows) where the library asks for one."""
+    out = _run_form(student, rec, weights, T, tail, True)
+    code = 1 if student.dtype == torch.bfloat16 else 0
+    if sv.load_library().specv_distill_workspace(code, *student.shape, rec["tokens"].shape[2]) > 0:
+        _run_form(student, rec, weights, T, tail, False)
+    return out
+
+
+def _run_form(student, rec, weights, T, tail, workspace):
     dev = {k: v.cuda() for k, v in rec.items()}
     w = None if weights is None else weights.cuda()
     kw = dict(weights=w, temperature=T, tail=tail)
     with sv.Verifier(1, 0, student.shape[2]) as v:
+        if not workspace:
+            _no_workspace(v)
         x = student.cuda()
         a = v.distill_loss(x, dev, **kw)
         g = v.distill_grad(x, dev, a["lse"], **kw)
@@ -187,10 +203,11 @@ def test_weights_left_out_and_one_row_alike(gpu, tail):
 
 @pytest.mark.parametrize("tail", ["bucket", "renorm"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_records_with_gaps_and_repeats(gpu, dtype, tail):
+@pytest.mark.parametrize("V", [2500, 100003])
+def test_records_with_gaps_and_repeats(gpu, dtype, tail, V):
     """Ignored tokens, the same token more than once, -inf logits, a record
     with one live entry."""
-    B, n, V, K = 4, 2, 2500, 12
+    B, n, K = 5, 2, 12
     t, s = _rows(17, B, n, V, dtype)
     rec = _record(t, K, 1.0)
     rec["tokens"][0, 0, 3] = -1
@@ -200,6 +217,8 @@ def test_records_with_gaps_and_repeats(gpu, dtype, tail):
     rec["logits"][1, 0, 6:] = -float("inf")
     rec["tokens"][1, 1, 1:] = -1
     rec["tokens"][2] = rec["tokens"][2, :1, :1]                     # all entries one token
+    rec["tokens"][4, 0, 1] = rec["tokens"][4, 0, 0]                 # twice, without a student's mass
+    s[4, 0, rec["tokens"][4, 0, 0].item()] = -float("inf")
     _run(s, rec, None, 1.0, tail)
 
 
@@ -294,9 +313,10 @@ def test_gradient_against_differences_of_the_kernel(gpu):
     assert (num - grad).abs().max() < 1.2e-3
 
 
-def test_large_offsets(gpu):
+@pytest.mark.parametrize("V", [3001, 100003])
+def test_large_offsets(gpu, V):
     """Rows past 2^31 elements of the first."""
-    V, K = 3001, 8
+    K = 8
     t, s = _rows(37, 3, 1, V, "bf16")
     rec = _record(t, K, 1.0)
     dev = {k: x.cuda() for k, x in rec.items()}
@@ -311,8 +331,9 @@ def test_large_offsets(gpu):
         assert torch.equal(x, want["grad"]) and torch.equal(got["loss"], want["loss"])
 
 
-def test_many_rows_repeat_bit_for_bit(gpu):
-    B, n, V, K = 30, 40, 2003, 16
+@pytest.mark.parametrize("B,n,V", [(30, 40, 2003), (30, 14, 40001), (12, 5, 100003)])
+def test_many_rows_repeat_bit_for_bit(gpu, B, n, V):
+    K = 16
     g = torch.Generator(device="cuda").manual_seed(5)
     x = (torch.randn(B, n, V, generator=g, device="cuda") * 3).to(torch.bfloat16)
     with sv.Verifier(1, 0, V) as v:
@@ -325,6 +346,25 @@ def test_many_rows_repeat_bit_for_bit(gpu):
         assert torch.equal(row["grad"], a["grad"][7:9]) and torch.equal(row["loss"], a["loss"][7:9])
         cpu = {k: y[7:9].cpu() for k, y in rec.items()}
         _check(x[7:9].cpu(), cpu, None, 1.0, "bucket", {"loss": row["loss"], "flags": row["flags"]}, row["grad"])
+
+
+def test_parts_and_whole_rows_agree(gpu):
+    """With and without a workspace: sums in another order, so within twice
+    the bounds above; here simply 2e-5 of the loss and of the largest gradient
+    (two float32 log-sum-exps of 50000 terms, 250 * 2^-24 each)."""
+    t, s = _rows(41, 3, 5, 50000, "f32")
+    rec = {k: x.cuda() for k, x in _record(t, 32, 1.3).items()}
+    with sv.Verifier(1, 0, 50000) as v:
+        a = v.distill_loss_grad(s.cuda(), rec, temperature=1.3)
+        l1 = v.distill_loss(s.cuda(), rec, temperature=1.3)
+        _no_workspace(v)
+        b = v.distill_loss_grad(s.cuda(), rec, temperature=1.3)
+        l2 = v.distill_loss(s.cuda(), rec, temperature=1.3)
+    for x in (l1["loss"], l2["loss"], b["loss"]):
+        assert ((a["loss"] - x).abs() <= 2e-5 * x.abs() + 2e-5).all()
+    assert ((a["loss"] - b["loss"]).abs() <= 2e-5 * b["loss"].abs() + 2e-5).all()
+    assert (a["grad"] - b["grad"]).abs().max() <= 2e-5 * b["grad"].abs().max()
+    assert (l1["lse"] - l2["lse"]).abs().max() <= 2e-5
 
 
 def test_binding_refusals(gpu):

@@ -109,14 +109,15 @@ def test_top_logits(lib, handle):
 
 def test_distill(lib, handle):
     def call(op, h=handle, x=P, sb=3000, sp=1000, dtype=0, B=2, n=3, V=1000, rec=True, tok=P, val=P, lse=P,
-             rsb=3, K=4, w=None, T=1.0, tail=1, loss=P, out=P, flags=None, g=P + (1 << 16), gsb=3000, gsp=1000):
+             rsb=3, K=4, w=None, T=1.0, tail=1, loss=P, out=P, flags=None, g=P + (1 << 16), gsb=3000, gsp=1000,
+             ws=None, wsn=0):
         r = sv._Teacher(tok, val, lse, rsb, K)
         a = (h, None, x, sb, sp, dtype, B, n, V, ctypes.byref(r) if rec else None, w, T, tail)
         if op == "loss":
-            return lib.specv_distill_loss(*a, loss, out, flags)
+            return lib.specv_distill_loss(*a, loss, out, flags, ws, wsn)
         if op == "grad":
             return lib.specv_distill_grad(*a, out, g, gsb, gsp)
-        return lib.specv_distill_loss_grad(*a, loss, flags, g, gsb, gsp)
+        return lib.specv_distill_loss_grad(*a, loss, flags, g, gsb, gsp, ws, wsn)
     for op in ("loss", "grad", "loss_grad"):
         assert call(op, h=None) == NULL and call(op, x=None) == NULL and call(op, rec=False) == NULL
         assert call(op, tok=None) == NULL and call(op, lse=None) == NULL
@@ -132,6 +133,21 @@ def test_distill(lib, handle):
         assert call(op, g=None) == NULL and call(op, gsp=-1) == SHAPE and call(op, gsp=10) == SHAPE
         assert call(op, g=P + 2) == ALIGN and call(op, g=P + 4) == SHAPE
         assert call(op, sb=0, sp=0, g=P, gsb=0, gsp=0) == SHAPE
+
+
+def test_distill_workspace(lib, handle):
+    size = lib.specv_distill_workspace
+    assert size(0, 2, 3, 50000, 8) > 0 and size(1, 1, 1, 128256, 256) > 0
+    assert size(0, 2, 3, 1000, 8) == 0 and size(0, 65, 1, 50000, 8) == 0 and size(1, 1 << 15, 1 << 15, 128256, 8) == 0 and size(1, 0, 3, 128256, 8) == 0
+    assert size(2, 2, 3, 50000, 8) == 0 and size(0, 2, 3, 50000, 257) == 0 and size(0, 2, 3, 1 << 20, 8) == 0
+    big = (ctypes.c_char * 65536)()
+    ctypes.memmove(big, ctypes.byref(sv._Config(0, 4, 5, 50000, 0)), ctypes.sizeof(sv._Config))
+    r = sv._Teacher(P, P, P, 3, 8)
+    need = size(0, 2, 3, 50000, 8)
+    for ws, n, status in ((P + 8, need, ALIGN), (P, need - 1, CAPACITY), (P, -1, CAPACITY), (P, 0, CAPACITY)):
+        a = (big, None, P, 150000, 50000, 0, 2, 3, 50000, ctypes.byref(r), None, 1.0, 1)
+        assert lib.specv_distill_loss(*a, P, P, None, ws, n) == status
+        assert lib.specv_distill_loss_grad(*a, P, None, P + (1 << 24), 150000, 50000, ws, n) == status
 
 
 def test_struct_layouts_match_the_binding(tmp_path):
