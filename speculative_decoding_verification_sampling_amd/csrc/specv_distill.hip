@@ -690,7 +690,7 @@ hipError_t launch_rows(const DistillArgs& a, hipStream_t stream, hipEvent_t* ev)
 #define SPECV_ROWS(NG, LD, MW) launch(k_distill<BF16, 1024, NG, LD, MW, OP, PAST>, rows, 1024, lds, stream, ev, a)
         if (full <= 4 * 1024) return SPECV_ROWS(4, 2, 8);
         if constexpr (BF16) return SPECV_ROWS(6, 2, 8);
-        else return full <= 16 * 1024 ? SPECV_ROWS(16, 4, 4) : SPECV_ROWS(20, 4, 4);
+        else return full <= 16 * 1024 ? SPECV_ROWS(16, 4, 4) : SPECV_ROWS(18, 4, 4);
 #undef SPECV_ROWS
     }
 }

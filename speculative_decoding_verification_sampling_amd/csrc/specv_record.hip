@@ -17,6 +17,7 @@ constexpr int kLoads = 4;                       // 16-byte groups a thread loads
 constexpr int kMaxBlocks = 8;                   // blocks per thread (their statistics stand in LDS)
 constexpr int kWaveBlk = 128;                   // blocks a wave reads again
 constexpr int kCandCap = 1024;                  // candidates ranked
+constexpr int kSortFrom = 320;                  // by a sort when there are more than this
 constexpr unsigned kLowestFinite = 0x00800000u; // the order key of -FLT_MAX; -inf lies below
 
 // Order key of a logit: larger key, larger value; -0 counts as +0.
@@ -41,6 +42,8 @@ struct RecordScratch {
     unsigned cnt[NW];
     unsigned digit, need, n;
 };
+
+__device__ inline float wave_min(float x) { return -wave_max(-x); }
 
 // (m, s) statistics joined across the wave.
 __device__ inline void wave_join_ms(float& m, float& s, float scale) {
@@ -80,6 +83,37 @@ __device__ inline void write_lse(const RecordArgs& a, float* olse, float mx, flo
 // leaves the values by rank; places behind the V-th get token -1.
 __device__ inline void rank_entries(const RecordArgs& a, int n, int keep, int* otok, float* oval,
                                     RecordScratch& sc) {
+    if (n > kSortFrom) {
+        // many: a bitonic sort, largest first (55 rounds for 1024; by counting the LDS reads grow as n^2)
+        const int P = n > 512 ? 1024 : 512;
+        static_assert(2 * NT >= kCandCap, "a pair a thread");
+        for (int t = n + (int)threadIdx.x; t < P; t += NT) sc.ent[t] = 0;
+#pragma unroll 1
+        for (int k = 2; k <= P; k *= 2)
+#pragma unroll 1
+            for (int j = k / 2; j > 0; j /= 2) {
+                __syncthreads();
+                const int t = 2 * (int)threadIdx.x - ((int)threadIdx.x & (j - 1));
+                if (t < P) {
+                    const unsigned long long x = sc.ent[t], y = sc.ent[t + j];
+                    if ((x < y) == ((t & k) == 0)) {
+                        sc.ent[t] = y;
+                        sc.ent[t + j] = x;
+                    }
+                }
+            }
+        __syncthreads();
+        for (int t = threadIdx.x; t < n; t += NT) {
+            const unsigned long long e = sc.ent[t];
+            const float x = key_value((unsigned)(e >> 32));
+            if (t < keep) {
+                otok[t] = (int)~(unsigned)e;
+                oval[t] = x;
+            }
+            sc.u.c.sorted[t] = x;
+        }
+        n = 0;                                        // done
+    }
     // an entry is compared by ``parts`` neighbouring lanes, as many as there are threads for
     int parts = 1;
     while (parts < 16 && n * parts * 2 <= NT) parts *= 2;
@@ -115,6 +149,23 @@ __device__ inline void rank_entries(const RecordArgs& a, int n, int keep, int* o
     __syncthreads();
 }
 
+// f(token, logit, whether there is one) for every entry of a row, by the whole
+// workgroup; all lanes of a wave call f together.
+template <bool BF16, typename F>
+__device__ __forceinline__ void each_entry(const RecordArgs& a, const void* row, F f) {
+    constexpr int G = RowGroup<BF16>::G;
+    const int full = a.V / G, groups = (a.V + G - 1) / G;
+#pragma unroll 1
+    for (int g0 = 0; g0 < groups; g0 += NT) {
+        const int g = g0 + (int)threadIdx.x;
+        RowGroup<BF16> x;
+        x.issue(row, g, full);
+        x.finish(row, g, full, a.V);
+#pragma unroll
+        for (int e = 0; e < G; ++e) f(g * G + e, x.elem(e), g * G + e < a.V);
+    }
+}
+
 // The record of a row whose candidates are too many (values equal or nearly
 // so, or unevenly spread): the K-th largest value by a radix select on order
 // keys, digit by digit over the row, then the entries above it and the first
@@ -131,17 +182,41 @@ __device__ __forceinline__ void record_by_digits(const RecordArgs& a, const void
         __syncthreads();
         for (int k = tid; k < kBins; k += NT) sc.u.hist[k] = 0;
         __syncthreads();
-        for (int v = tid; v < a.V; v += NT) {
-            const unsigned key = order_key(load_elem<BF16>(row, v));
-            if ((key & mask) == prefix) atomicAdd(&sc.u.hist[(key >> shift) & ((1u << bits) - 1)], 1u);
-        }
+        each_entry<BF16>(a, row, [&](int, float x, bool in) {
+            const unsigned key = order_key(x);
+            in = in && (key & mask) == prefix;
+            const unsigned digit = (key >> shift) & ((1u << bits) - 1);
+            // the first lane's digit in one addition: rows of few values would queue up at one bin
+            const unsigned long long on = __ballot(in);
+            if (!on) return;
+            const unsigned d0 = __builtin_amdgcn_readlane(digit, __builtin_ctzll(on));
+            const unsigned long long same = __ballot(in && digit == d0);
+            if (lane == 0) atomicAdd(&sc.u.hist[d0], (unsigned)__popcll(same));
+            if (in && digit != d0) atomicAdd(&sc.u.hist[digit], 1u);
+        });
         __syncthreads();
-        if (tid == 0) {
-            unsigned left = need;
-            int k = (1 << bits) - 1;
-            while (sc.u.hist[k] < left) left -= sc.u.hist[k--];
-            sc.digit = (unsigned)k;
-            sc.need = left;
+        // the bin that holds the need-th key from the top: four bins a thread, the highest first
+        int c[kBins / NT], mine = 0;
+#pragma unroll
+        for (int u = 0; u < kBins / NT; ++u) {
+            c[u] = (int)sc.u.hist[kBins - 1 - (tid * (kBins / NT) + u)];
+            mine += c[u];
+        }
+        const int incl = wave_scan_incl(mine);
+        if (lane == kWave - 1) sc.cnt[wave] = (unsigned)incl;
+        __syncthreads();
+        int before = incl - mine;
+        for (int w = 0; w < wave; ++w) before += (int)sc.cnt[w];
+        if (before < (int)need && before + mine >= (int)need) {
+            int left = (int)need - before, u = 0;
+#pragma unroll
+            for (int k = 0; k < kBins / NT - 1; ++k)
+                if (u == k && c[k] < left) {
+                    left -= c[k];
+                    ++u;
+                }
+            sc.digit = (unsigned)(kBins - 1 - (tid * (kBins / NT) + u));
+            sc.need = (unsigned)left;
         }
         __syncthreads();
         prefix |= sc.digit << shift;
@@ -157,8 +232,8 @@ __device__ __forceinline__ void record_by_digits(const RecordArgs& a, const void
     __syncthreads();
     float s = 0.f, below = -kInf;
     unsigned ties = 0;
-    for (int v = tid; v < a.V; v += NT) {
-        const float x = load_elem<BF16>(row, v);
+    each_entry<BF16>(a, row, [&](int v, float x, bool in) {
+        if (!in) return;
         const unsigned key = order_key(x);
         if (key > kth) {
             sc.ent[atomicAdd(&sc.n, 1u)] = ((unsigned long long)key << 32) | ~(unsigned)v;
@@ -168,7 +243,7 @@ __device__ __forceinline__ void record_by_digits(const RecordArgs& a, const void
             s += fast_exp2((x - zk) * a.scale);
             below = fmaxf(below, x);
         }
-    }
+    });
     float rest = block_sum(s, sc.red) + (block_sum((float)ties, sc.red2) - (float)need);
     float ref = zk;
     if (rest == 0.f) {
@@ -256,17 +331,12 @@ __global__ __launch_bounds__(NT) void k_top_logits(RecordArgs a) {
 #pragma unroll
             for (int l = 0; l < kLoads; ++l) r[l].clear((t * kLoads + l) * NT + tid, full);
         }
-        float m = -kInf, s = 0.f;
+        float m = -kInf;
 #pragma unroll
         for (int l = 0; l < kLoads; ++l)
 #pragma unroll
             for (int e = 0; e < G; ++e) m = fmaxf(m, r[l].elem(e));
-        // relative to the maximum before the scaling: a row of the type's lowest value stays finite
-        const float ref = m == -kInf ? 0.f : m;
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-#pragma unroll
-            for (int e = 0; e < G; ++e) s += fast_exp2((r[l].elem(e) - ref) * a.scale);
+        float s = sum_exp<kLoads>(r, ExpRef(m, a.scale));
         if (t >= whole && full * G < a.V && full >= t * kLoads * NT && (full - t * kLoads * NT) % NT == tid) {
             // the row's last, partial group: its place was cleared above
 #pragma unroll 1
@@ -292,19 +362,27 @@ __global__ __launch_bounds__(NT) void k_top_logits(RecordArgs a) {
         }
     }
 
-    // the bound: 16 bits of the wave's k-th largest lane maximum, then the
-    // smallest of the waves' (of those that hold 64 groups, if there are any)
-    const int waves = max(1, min(NW, groups / kWave));
-    const int k_wave = (K + waves - 1) / waves;
+    // the bound: 16 bits of the wave's k-th largest lane maximum, k its share
+    // of K by the groups it holds (rounded up), then the smallest of the waves'
+    const int held = groups / NT * kWave + min(max(groups % NT - wave * kWave, 0), kWave);
+    const int k_wave = (int)(((long long)K * held + groups - 1) / groups);
     const unsigned u0 = order_key(key0) >> 16, u1 = order_key(key1) >> 16;
-    unsigned bound = 0;
+    // (bits that all lanes share need no count)
+    float mx = wave_max(fmaxf(key0, key1));
+    const unsigned hi = order_key(mx) >> 16;
+    const unsigned lo = order_key(wave_min(a.blocks > 1 ? fminf(key0, key1) : key0)) >> 16;
+    unsigned bit = 0x8000u, bound = 0;
+    if (k_wave <= (a.blocks > 1 ? 2 * kWave : kWave)) {
+        bit = hi == lo ? 0u : 0x80000000u >> __builtin_clz(hi ^ lo);
+        bound = hi & ~(2 * bit - 1);
+        if (hi == lo) bound = hi;
+    }
 #pragma unroll 1
-    for (unsigned bit = 0x8000u; bit; bit >>= 1) {
+    for (; bit; bit >>= 1) {
         const unsigned c = bound | bit;
         if (__popcll(__ballot(u0 >= c)) + __popcll(__ballot(u1 >= c)) >= k_wave) bound = c;
     }
-    if (wave >= waves) bound = 0xFFFFu;
-    float mx = wave_max(fmaxf(key0, key1));
+    if (k_wave == 0) bound = 0xFFFFu;
     const bool wave_bad = __ballot(bad) != 0;
     if (lane == 0) {
         sc.red[wave] = mx;
