@@ -13,12 +13,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "specv_device.hpp"
 
 namespace specv {
 namespace {
 
 constexpr int kTok = 8;                        // tokens per thread: one byte of a bit row
+constexpr long long kFill = 1024;              // workgroups below which positions are split
 constexpr int kAdjChunk = kBlock * kTok;       // tokens per workgroup
 
 // 8 logits as they are stored.
@@ -99,21 +102,23 @@ struct Group<false> {
 
 // The biases of batch row b on this thread's tokens v .. v + 7 (added in list
 // order into sum[]); returns their bits.  Every wave walks the row's entries
-// 64 at a time and stops only at those inside the chunk, so the workgroup
+// 64 at a time and stops only at those among its own tokens, so the workgroup
 // needs no LDS and no barrier for them.
-__device__ __forceinline__ unsigned gather_bias(const AdjustArgs& a, int b, int v0, int len, float (&sum)[kTok]) {
-    const int tid = threadIdx.x, lane = tid % kWave;
+__device__ __forceinline__ unsigned gather_bias(const AdjustArgs& a, int b, int v0, float (&sum)[kTok]) {
+    const int lane = threadIdx.x % kWave;
+    const int first = v0 + ((int)threadIdx.x - lane) * kTok;                 // the wave's tokens
+    const int len = min(kWave * kTok, a.V - first);
     const int lo = min(max(a.bias_off[b], 0), a.n_bias), hi = min(max(a.bias_off[b + 1], 0), a.n_bias);
     unsigned bits = 0;
     for (int base = lo; base < hi; base += kWave) {
         const int i = min(base + lane, hi - 1);
         const int t = a.bias_tok[i];
         const float val = a.bias_val[i];
-        unsigned long long m = __ballot(base + lane < hi && t >= v0 && t - v0 < len);
+        unsigned long long m = __ballot(base + lane < hi && t >= first && t - first < len);
         while (m) {
             const int k = __builtin_ctzll(m);
             m &= m - 1;
-            const int rel = __builtin_amdgcn_readlane(t, k) - v0 - tid * kTok;
+            const int rel = __builtin_amdgcn_readlane(t, k) - first - lane * kTok;
             const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(val), k));
 #pragma unroll
             for (int e = 0; e < kTok; ++e)
@@ -200,7 +205,7 @@ __global__ __launch_bounds__(kBlock, 8) void k_adjust(AdjustArgs a) {
         }
         if (a.tokens) tok = a.tokens + (long long)b * a.tok_sb;
     }
-    const unsigned biased = a.bias_off ? gather_bias(a, b, v0, len, bias) : 0;
+    const unsigned biased = a.bias_off ? gather_bias(a, b, v0, bias) : 0;
     const float inv = 1.f / rep;
 
     int p = 0;                                                  // drafts taken into the counts so far
@@ -313,7 +318,11 @@ hipError_t launch(void (*fn)(A...), long long blocks, int threads, hipStream_t s
 
 hipError_t launch_adjust(AdjustArgs& a, bool bf16, hipStream_t stream, hipEvent_t* ev) {
     a.C = (a.V + kAdjChunk - 1) / kAdjChunk;
-    a.pp = a.n;
+    // a workgroup takes all positions of its tokens (64 x 6 rows of 128256: 61 us, one
+    // position each 100) unless there are too few to fill the device
+    const long long wgs = (long long)a.B * a.C;
+    const int groups = (int)std::min<long long>(a.n, (kFill + wgs - 1) / wgs);
+    a.pp = (a.n + groups - 1) / groups;
     a.PG = (a.n + a.pp - 1) / a.pp;
     const bool inplace = a.in == a.out;
     auto fn = bf16 ? (inplace ? k_adjust<true, true> : k_adjust<true, false>)

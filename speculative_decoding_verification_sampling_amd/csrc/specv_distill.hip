@@ -330,14 +330,17 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
     Teacher t{};
     if (wave == 0) {
         t = take_teacher(a, rec, sc);
-        float ms, ss;
-        const bool bad_s = take_student(a, sc, ms, ss);
         if (lane == 0) {
             sc.P = t.P;
             sc.p_rest = t.p_rest;
+            sc.ok = t.ok;
+        }
+    } else if (wave == 1) {
+        float ms, ss;
+        const bool bad_s = take_student(a, sc, ms, ss);
+        if (lane == 0) {
             sc.m_s = ms;
             sc.s_s = ss;
-            sc.ok = t.ok;
             sc.bad = bad_s;
         }
     }
@@ -685,12 +688,14 @@ hipError_t launch_rows(const DistillArgs& a, hipStream_t stream, hipEvent_t* ev)
     (void)full;
     if constexpr (OP == kDistillGrad) return launch(k_part_grad<BF16, false, PAST>, rows * a.parts, kBlock, 0, stream, ev, a);
     else if constexpr (OP == kDistillLoss)
-        return launch(k_distill<BF16, 512, 0, 4, 4, OP, PAST>, rows, 512, lds, stream, ev, a);
+        return full <= 1024 ? launch(k_distill<BF16, 256, 0, 4, 4, OP, PAST>, rows, 256, lds, stream, ev, a)
+                            : launch(k_distill<BF16, 512, 0, 4, 4, OP, PAST>, rows, 512, lds, stream, ev, a);
     else {
-#define SPECV_ROWS(NG, LD, MW) launch(k_distill<BF16, 1024, NG, LD, MW, OP, PAST>, rows, 1024, lds, stream, ev, a)
-        if (full <= 4 * 1024) return SPECV_ROWS(4, 2, 8);
-        if constexpr (BF16) return SPECV_ROWS(6, 2, 8);
-        else return full <= 16 * 1024 ? SPECV_ROWS(16, 4, 4) : SPECV_ROWS(18, 4, 4);
+#define SPECV_ROWS(NT, NG, LD, MW) launch(k_distill<BF16, NT, NG, LD, MW, OP, PAST>, rows, NT, lds, stream, ev, a)
+        if (full <= 4 * 256) return SPECV_ROWS(256, 4, 2, 8);
+        if (full <= 4 * 1024) return SPECV_ROWS(1024, 4, 2, 8);
+        if constexpr (BF16) return SPECV_ROWS(1024, 6, 2, 8);
+        else return full <= 16 * 1024 ? SPECV_ROWS(1024, 16, 4, 4) : SPECV_ROWS(1024, 18, 4, 4);
 #undef SPECV_ROWS
     }
 }
