@@ -428,14 +428,24 @@ __global__ __launch_bounds__(NT) void k_top_logits(RecordArgs a) {
     if (n_blk > kWaveBlk) {
         if (lane == 0) atomicAdd(&sc.n, kCandCap + 1u);              // too many: the other way, below
     } else {
+        const int reads = n_blk * per_blk;
+        const auto group = [&](int k) {                              // the k-th group to read, past the end: none
+            if (k >= reads) return groups;
+            const int q = a.reps == 1 ? k / kLoads : k / per_blk;
+            const int id = sc.u.c.blk[wave][q];
+            return ((id / NT) * per_blk + k - q * per_blk) * NT + id % NT;
+        };
+        int next = group(lane);
+        RowGroup<BF16> nx;
+        nx.issue(row, next, full);
 #pragma unroll 1
-        for (int k0 = 0; k0 < n_blk * per_blk; k0 += kWave) {
-            const int k = k0 + lane;
-            const bool on = k < n_blk * per_blk;
-            const int id = on ? sc.u.c.blk[wave][k / per_blk] : 0;
-            const int g = on ? ((id / NT) * per_blk + k % per_blk) * NT + id % NT : groups;
-            RowGroup<BF16> x;
-            x.issue(row, g, full);
+        for (int k0 = 0; k0 < reads; k0 += kWave) {
+            const int g = next;
+            RowGroup<BF16> x = nx;
+            if (k0 + kWave < reads) {
+                next = group(k0 + kWave + lane);
+                nx.issue(row, next, full);
+            }
             x.finish(row, g, full, a.V);                             // past the end: -inf
             float gm = -kInf, gs = 0.f;
             int mine = 0;
