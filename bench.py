@@ -78,6 +78,8 @@ TRAFFIC_FILES = {
     ("truncated", "k_verify"): os.path.join(ROOT, "profiles", "traffic_k_verify_truncated.json"),
     ("mixed", "k_verify"): os.path.join(ROOT, "profiles", "traffic_k_verify_mixed.json"),
 }
+UNHASHED = ("specv_api.hip", "specv_measure.hip", "specv_logits_api.hip", "specv_logits.hpp",
+            "specv_logits_device.hpp", "specv_adjust.hip", "specv_record.hip", "specv_distill.hip")
 HOST_POOL_CAP = 16          # worker processes: the host share of one GPU
 
 
@@ -105,13 +107,13 @@ def sampler_bytes(B, V, es):
 
 
 def kernel_source_hash():
-    """Hash of the device-code sources (every file under csrc/ except the
-    host-side C ABI and the measurement aid), so that counter figures are
-    dropped once a kernel changes."""
+    """Hash of the verify and draft-sampler device code (every file under csrc/
+    except the host-side C ABI, the measurement aid and the logits operators'
+    own files), so that counter figures are dropped once a kernel changes."""
     h = hashlib.sha256()
     d = os.path.dirname(KERNEL_SRC)
     for name in sorted(os.listdir(d)):
-        if name in ("specv_api.hip", "specv_measure.hip") or not name.endswith((".hip", ".hpp")):
+        if name in UNHASHED or not name.endswith((".hip", ".hpp")):
             continue
         with open(os.path.join(d, name), "rb") as f:
             h.update(name.encode() + f.read())

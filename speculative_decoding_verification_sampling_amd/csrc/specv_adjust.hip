@@ -15,7 +15,7 @@
 
 #include <algorithm>
 
-#include "specv_device.hpp"
+#include "specv_logits_device.hpp"
 
 namespace specv {
 namespace {
@@ -143,7 +143,7 @@ __device__ inline float divide(float x, float d, float inv) {
 // mask leaves nothing is not read).  In place only the groups that change are
 // read and written.
 template <bool BF16, bool INPLACE>
-__global__ __launch_bounds__(kBlock, 8) void k_adjust(AdjustArgs a) {
+__global__ __launch_bounds__(kBlock, BF16 ? 8 : 7) void k_adjust(AdjustArgs a) {
     constexpr int kAhead = 2;
     const int tid = threadIdx.x;
     const unsigned per_row = (unsigned)a.C * a.PG;

@@ -13,6 +13,7 @@
 
 #include "specv.h"
 #include "specv_internal.hpp"
+#include "specv_logits.hpp"
 
 struct specv_ctx {
     specv_config cfg;

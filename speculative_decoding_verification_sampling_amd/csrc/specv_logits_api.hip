@@ -7,7 +7,7 @@
 #include <stdint.h>
 
 #include "specv.h"
-#include "specv_internal.hpp"
+#include "specv_logits.hpp"
 
 namespace {
 

@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "specv_device.hpp"
+#include "specv_logits_device.hpp"
 
 namespace specv {
 namespace {
