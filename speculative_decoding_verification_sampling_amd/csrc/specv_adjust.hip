@@ -107,36 +107,48 @@ struct Group<false> {
     }
 };
 
-// The biases of batch row b on this thread's tokens v .. v + 7 (added in list
+// The biases of a batch row on this thread's tokens v .. v + 7 (added in list
 // order into sum[]); returns their bits.  Every wave walks the row's entries
 // 64 at a time and stops only at those among its own tokens, so the workgroup
-// needs no LDS and no barrier for them.
-__device__ __forceinline__ unsigned gather_bias(const AdjustArgs& a, int b, int v0, float (&sum)[kTok]) {
-    const int lane = threadIdx.x % kWave;
-    const int first = v0 + ((int)threadIdx.x - lane) * kTok;                 // the wave's tokens
-    const int len = min(kWave * kTok, a.V - first);
-    const int lo = min(max(a.bias_off[b], 0), a.n_bias), hi = min(max(a.bias_off[b + 1], 0), a.n_bias);
-    unsigned bits = 0;
-    for (int base = lo; base < hi; base += kWave) {
-        const int i = min(base + lane, hi - 1);
-        const int t = a.bias_tok[i];
-        const float val = a.bias_val[i];
-        unsigned long long m = __ballot(base + lane < hi && t >= first && t - first < len);
-        while (m) {
-            const int k = __builtin_ctzll(m);
-            m &= m - 1;
-            const int rel = __builtin_amdgcn_readlane(t, k) - first - lane * kTok;
-            const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(val), k));
-#pragma unroll
-            for (int e = 0; e < kTok; ++e)
-                if (rel == e) {
-                    sum[e] += x;
-                    bits |= 1u << e;
-                }
-        }
+// needs no LDS and no barrier for them.  ``issue`` loads the first 64, to be
+// on their way with other loads.
+struct BiasEntries {
+    int lo, hi, tok;
+    float val;
+    __device__ __forceinline__ void load(const AdjustArgs& a, int base) {
+        const int i = min(base + (int)threadIdx.x % kWave, hi - 1);
+        tok = a.bias_tok[i];
+        val = a.bias_val[i];
     }
-    return bits;
-}
+    __device__ __forceinline__ void issue(const AdjustArgs& a, int b) {
+        lo = min(max(a.bias_off[b], 0), a.n_bias);
+        hi = min(max(a.bias_off[b + 1], 0), a.n_bias);
+        if (lo < hi) load(a, lo);
+    }
+    __device__ __forceinline__ unsigned gather(const AdjustArgs& a, int v0, float (&sum)[kTok]) {
+        const int lane = threadIdx.x % kWave;
+        const int first = v0 + ((int)threadIdx.x - lane) * kTok;             // the wave's tokens
+        const int len = min(kWave * kTok, a.V - first);
+        unsigned bits = 0;
+        for (int base = lo; base < hi; base += kWave) {
+            if (base > lo) load(a, base);
+            unsigned long long m = __ballot(base + lane < hi && tok >= first && tok - first < len);
+            while (m) {
+                const int k = __builtin_ctzll(m);
+                m &= m - 1;
+                const int rel = __builtin_amdgcn_readlane(tok, k) - first - lane * kTok;
+                const float x = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(val), k));
+#pragma unroll
+                for (int e = 0; e < kTok; ++e)
+                    if (rel == e) {
+                        sum[e] += x;
+                        bits |= 1u << e;
+                    }
+            }
+        }
+        return bits;
+    }
+};
 
 // x / d, correctly rounded, from inv = 1 / d correctly rounded: the quotient's
 // remainder corrects it once.  An infinite or NaN quotient stays.
@@ -192,6 +204,9 @@ __global__ __launch_bounds__(kBlock, BF16 ? 8 : 7) void k_adjust(AdjustArgs a) {
     load_masks(i0);
     if (!INPLACE) load_rows(i0, 0);                             // on their way during the preparations
 
+    BiasEntries be;
+    if (a.bias_off) be.issue(a, b);
+
     float rep = 1.f, pres = 0.f, freq = 0.f;
     unsigned used = 0;
     float cnt[kTok], bias[kTok];
@@ -208,14 +223,23 @@ __global__ __launch_bounds__(kBlock, BF16 ? 8 : 7) void k_adjust(AdjustArgs a) {
             used = reinterpret_cast<const unsigned char*>(a.seen + p.slot * words)[v / 8] & live;
             const int* cr = a.counts + (long long)p.slot * a.V + v;
             if (used) {
+                // all of them at once: one load each, converted where it lands, would wait eight times
+                int ci[kTok];
+                if (m == kTok) {
+                    const u32x4 lo = *reinterpret_cast<const u32x4_a2*>(cr), hi = *reinterpret_cast<const u32x4_a2*>(cr + 4);
 #pragma unroll
-                for (int e = 0; e < kTok; ++e)
-                    if ((used >> e) & 1) cnt[e] = (float)cr[e];
+                    for (int e = 0; e < kTok; ++e) ci[e] = (int)(e < 4 ? lo[e] : hi[e - 4]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kTok; ++e) ci[e] = cr[min(e, m - 1)];
+                }
+#pragma unroll
+                for (int e = 0; e < kTok; ++e) cnt[e] = (used >> e) & 1 ? (float)ci[e] : 0.f;
             }
         }
         if (a.tokens) tok = a.tokens + (long long)b * a.tok_sb;
     }
-    const unsigned biased = a.bias_off ? gather_bias(a, b, v0, bias) : 0;
+    const unsigned biased = a.bias_off ? be.gather(a, v0, bias) : 0;
     const float inv = 1.f / rep;
 
     int p = 0;                                                  // drafts taken into the counts so far
