@@ -84,6 +84,23 @@ __device__ inline void finish_entries(const DistillArgs& a, Entries& r) {
     }
 }
 
+// The student's logits of the entries whose token lies in [v0, v1), -inf for
+// the others: all loads first, so that they wait once.
+template <bool BF16>
+__device__ inline void load_logits(const void* row, const Entries& r, int v0, int v1, float (&z)[kE]) {
+    unsigned raw[kE];
+#pragma unroll
+    for (int u = 0; u < kE; ++u) {
+        raw[u] = BF16 ? 0xFF80u : 0xFF800000u;
+        if (r.tok[u] >= v0 && r.tok[u] < v1) {
+            if constexpr (BF16) raw[u] = static_cast<const unsigned short*>(row)[r.tok[u]];
+            else raw[u] = static_cast<const unsigned*>(row)[r.tok[u]];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kE; ++u) z[u] = __uint_as_float(BF16 ? raw[u] << 16 : raw[u]);
+}
+
 // The teacher's side, in one wave: the probabilities of the entries (sc.p)
 // and of the rest.
 struct Teacher {
@@ -261,6 +278,7 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
     for (int k = tid; k < (a.V + 31) / 32; k += NT) inside[k] = 0;
     if (tid == 0) sc.twice = 0;
     __syncthreads();
+    float z[kE];
     if (wave == 0) {
         finish_entries(a, r);
 #pragma unroll
@@ -268,18 +286,19 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
             const int k = lane + u * kWave;
             if (k >= a.K) continue;
             int rep = 0;
-            float z = -kInf;
             if (r.tok[u] >= 0) {
                 const unsigned bit = 1u << (r.tok[u] % 32);
                 rep = !(atomicOr(&inside[r.tok[u] / 32], bit) & bit);
                 if (!rep) sc.twice = 1;
-                z = load_elem<BF16>(row, r.tok[u]);
             }
             sc.tok[k] = r.tok[u];
             sc.t[k] = r.t[u];
             sc.rep[k] = rep;
-            sc.z[k] = z;
         }
+        load_logits<BF16>(row, r, 0, a.V, z);
+#pragma unroll
+        for (int u = 0; u < kE; ++u)
+            if (lane + u * kWave < a.K) sc.z[lane + u * kWave] = z[u];
     }
     __syncthreads();
 
@@ -447,6 +466,8 @@ __global__ __launch_bounds__(kBlock) void k_part_stats(DistillArgs a, bool skip)
     float* z = a.zs + ri * 2 * a.K;
     if (wave == 0) {
         finish_entries(a, r);
+        float x[kE];
+        load_logits<BF16>(row, r, v0, v1, x);
 #pragma unroll
         for (int u = 0; u < kE; ++u) {
             const int k = lane + u * kWave, t = r.tok[u];
@@ -454,8 +475,7 @@ __global__ __launch_bounds__(kBlock) void k_part_stats(DistillArgs a, bool skip)
             if (t >= v0 && t < v1) {
                 const unsigned bit = 1u << (t % 32);
                 const bool rep = !(atomicOr(&mark[(t - v0) / 32], bit) & bit);
-                const float x = load_elem<BF16>(row, t);
-                z[k] = x;
+                z[k] = x[u];
                 z[a.K + k] = rep ? 1.f : 0.f;
             } else if (t < 0 && part == 0) {
                 z[k] = -kInf;
@@ -602,6 +622,8 @@ __global__ __launch_bounds__(kBlock) void k_part_grad(DistillArgs a) {
             rs = m_all;
         } else {
             finish_entries(a, r);
+            float z[kE];
+            load_logits<BF16>(row, r, v0, v1, z);
 #pragma unroll
             for (int u = 0; u < kE; ++u) {
                 const int k = lane + u * kWave, tk = r.tok[u];
@@ -611,7 +633,7 @@ __global__ __launch_bounds__(kBlock) void k_part_grad(DistillArgs a) {
                 if (tk >= v0 && tk < v1) {
                     const unsigned bit = 1u << (tk % 32);
                     if (atomicOr(&mark[(tk - v0) / 32], bit) & bit) sc.twice = 1;
-                    sc.z[k] = load_elem<BF16>(row, tk);
+                    sc.z[k] = z[u];
                 }
             }
             t = take_teacher(a, rec, sc);
