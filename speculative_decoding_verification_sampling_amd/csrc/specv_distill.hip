@@ -195,18 +195,6 @@ __device__ inline float token_p(const DistillArgs& a, const DistillScratch& sc, 
     return p;
 }
 
-// Statistics of G entries, those of S (bits of ``in``) left out.
-template <bool BF16>
-__device__ __forceinline__ void leave_out(RowGroup<BF16>& r, unsigned in) {
-    constexpr int G = RowGroup<BF16>::G;
-#pragma unroll
-    for (int e = 0; e < G; ++e) {
-        if (!((in >> e) & 1)) continue;
-        if constexpr (BF16) r.q[e / 2] = (e & 1) ? ((r.q[e / 2] & 0xFFFFu) | 0xFF800000u) : ((r.q[e / 2] & 0xFFFF0000u) | 0xFF80u);
-        else r.q[e] = 0xFF800000u;
-    }
-}
-
 // A group's gradient outside S: c exp2((x - ref) scale), or 0 for a row left
 // out (whose logits may be anything).
 template <typename Group>
@@ -310,7 +298,7 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
             const int g = j * NT + tid;
             if ((j + 1) * NT > full) h[j].clear(g, full);
             const unsigned in = g < full ? group_bits<BF16>(inside, g) : 0;
-            if (__ballot(in != 0)) leave_out<BF16>(h[j], in);    // for good: S is written over the rest at the end
+            if (__ballot(in != 0)) leave_out(h[j], in);    // for good: S is written over the rest at the end
 #pragma unroll
             for (int e = 0; e < G; ++e) m = fmaxf(m, h[j].elem(e));
         }
@@ -333,7 +321,7 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
                 const int g = (j + l) * NT + tid;
                 x[l].clear(g, full);
                 const unsigned in = g < full ? group_bits<BF16>(inside, g) : 0;
-                if (__ballot(in != 0)) leave_out<BF16>(x[l], in);
+                if (__ballot(in != 0)) leave_out(x[l], in);
 #pragma unroll
                 for (int e = 0; e < G; ++e) gm = fmaxf(gm, x[l].elem(e));
             }
@@ -490,7 +478,7 @@ __global__ __launch_bounds__(kBlock) void k_part_stats(DistillArgs a, bool skip)
         const int g = g0 + l * kBlock + tid;
         h[l].clear(g, full);
         const unsigned in = g < full ? group_bits<BF16>(mark, g - g0) : 0;
-        if (__ballot(in != 0)) leave_out<BF16>(h[l], in);
+        if (__ballot(in != 0)) leave_out(h[l], in);
 #pragma unroll
         for (int e = 0; e < G; ++e) m = fmaxf(m, h[l].elem(e));
     }

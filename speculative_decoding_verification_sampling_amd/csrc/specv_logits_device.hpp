@@ -58,6 +58,14 @@ struct RowGroup {
         if constexpr (BF16) return (e & 1) ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
         else return __uint_as_float(q[e]);
     }
+    // Entry e for a per-lane e.
+    __device__ inline float elem_dyn(int e) const {
+        constexpr int P = G / 4;                  // entries of a word
+        const unsigned lo = e < P ? q[0] : q[1], hi = e < 3 * P ? q[2] : q[3];
+        const unsigned w = e < 2 * P ? lo : hi;
+        if constexpr (BF16) return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
+        else return __uint_as_float(w);
+    }
     // Keeps the group packed between two passes over it: the compiler would
     // otherwise unpack it once and hold the floats, twice the registers.
     __device__ inline void pin() { asm volatile("" : "+v"(q)); }
@@ -82,6 +90,18 @@ struct RowGroup {
         __builtin_nontemporal_store(q, static_cast<u32x4_a2*>(row) + g);
     }
 };
+
+// The entries named by the bits of ``in`` become -inf.
+template <bool BF16>
+__device__ __forceinline__ void leave_out(RowGroup<BF16>& r, unsigned in) {
+    constexpr int G = RowGroup<BF16>::G;
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+        if (!((in >> e) & 1)) continue;
+        if constexpr (BF16) r.q[e / 2] = (e & 1) ? ((r.q[e / 2] & 0xFFFFu) | 0xFF800000u) : ((r.q[e / 2] & 0xFFFF0000u) | 0xFF80u);
+        else r.q[e] = 0xFF800000u;
+    }
+}
 
 // exp2((x - ref) * scale) for many x and one ref, as one fused multiply-add
 // each: 2^(x scale - R) with R = ref scale rounded, and the factor

@@ -26,8 +26,7 @@ constexpr int kLoads = 4;                       // 16-byte groups a thread loads
 constexpr int kMaxBlocks = 8;                   // blocks per thread (their statistics stand in LDS)
 constexpr int kWaveBlk = 128;                   // blocks a wave reads again
 constexpr int kCandCap = 1024;                  // candidates ranked
-constexpr int kSortFrom = 320;                  // by a sort when there are more than this (1001 candidates
-                                                // a row, 384 rows: 75 us by counting, 26 by the sort)
+constexpr int kSortFrom = 192;                  // by sorted lists when there are more than this
 constexpr unsigned kLowestFinite = 0x00800000u; // the order key of -FLT_MAX; -inf lies below
 
 // Order key of a logit: larger key, larger value; -0 counts as +0.
@@ -94,35 +93,50 @@ __device__ inline void write_lse(const RecordArgs& a, float* olse, float mx, flo
 __device__ inline void rank_entries(const RecordArgs& a, int n, int keep, int* otok, float* oval,
                                     RecordScratch& sc) {
     if (n > kSortFrom) {
-        // many: a bitonic sort, largest first (55 rounds for 1024; by counting the LDS reads grow as n^2)
-        const int P = n > 512 ? 1024 : 512;
-        static_assert(2 * NT >= kCandCap, "a pair a thread");
-        for (int t = n + (int)threadIdx.x; t < P; t += NT) sc.ent[t] = 0;
+        // many: every wave sorts 64 entries in registers, largest first, and an entry's rank is
+        // its place in its own list plus, by binary search, its places in the others
+        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, lists = (n + kWave - 1) / kWave;
+        constexpr int kOwn = kCandCap / NT;                           // lists of a wave
+        unsigned long long own[kOwn];
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u) {
+            const int l = wave + u * NW, t = l * kWave + lane;
+            if (l >= lists) break;
+            unsigned long long e = t < n ? sc.ent[t] : 0;
 #pragma unroll 1
-        for (int k = 2; k <= P; k *= 2)
+            for (int k = 2; k <= kWave; k *= 2)
 #pragma unroll 1
-            for (int j = k / 2; j > 0; j /= 2) {
-                __syncthreads();
-                const int t = 2 * (int)threadIdx.x - ((int)threadIdx.x & (j - 1));
-                if (t < P) {
-                    const unsigned long long x = sc.ent[t], y = sc.ent[t + j];
-                    if ((x < y) == ((t & k) == 0)) {
-                        sc.ent[t] = y;
-                        sc.ent[t + j] = x;
-                    }
+                for (int d = k / 2; d > 0; d /= 2) {
+                    const unsigned long long o = __shfl_xor(e, d);
+                    const bool larger = ((lane & d) == 0) == ((lane & k) == 0);    // which of the two stays here
+                    e = (e > o) == larger ? e : o;
                 }
-            }
-        __syncthreads();
-        for (int t = threadIdx.x; t < n; t += NT) {
-            const unsigned long long e = sc.ent[t];
-            const float x = key_value((unsigned)(e >> 32));
-            if (t < keep) {
-                otok[t] = (int)~(unsigned)e;
-                oval[t] = x;
-            }
-            sc.u.c.sorted[t] = x;
+            own[u] = e;
+            sc.ent[t] = e;
         }
-        n = 0;                                        // done
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kOwn; ++u) {
+            const int l = wave + u * NW;
+            if (l >= lists || own[u] == 0) break;
+            int rank = lane;
+#pragma unroll 4
+            for (int q = 0; q < lists; ++q) {
+                const unsigned long long* o = sc.ent + q * kWave;
+                int at = 0;                                           // entries of the list that are larger
+#pragma unroll
+                for (int d = kWave / 2; d > 0; d /= 2) at += o[at + d - 1] > own[u] ? d : 0;
+                at += o[at] > own[u];
+                rank += q == l ? 0 : at;
+            }
+            const float x = key_value((unsigned)(own[u] >> 32));
+            if (rank < keep) {
+                otok[rank] = (int)~(unsigned)own[u];
+                oval[rank] = x;
+            }
+            sc.u.c.sorted[rank] = x;
+        }
+        n = 0;                                                        // done
     }
     // an entry is compared by ``parts`` neighbouring lanes, as many as there are threads for
     int parts = 1;
@@ -457,28 +471,25 @@ __global__ __launch_bounds__(NT) void k_top_logits(RecordArgs a) {
                 nx.issue(row, next, full);
             }
             x.finish(row, g, full, a.V);                             // past the end: -inf
-            float gm = -kInf, gs = 0.f;
-            int mine = 0;
+            unsigned in = 0;
 #pragma unroll
-            for (int e = 0; e < G; ++e) {
-                if (x.elem(e) >= L) ++mine;
-                else gm = fmaxf(gm, x.elem(e));
-            }
-            const int incl = wave_scan_incl(mine);
+            for (int e = 0; e < G; ++e) in |= x.elem(e) >= L ? 1u << e : 0u;
+            const int mine = __popc(in), incl = wave_scan_incl(mine);
             unsigned base = 0;
             if (lane == kWave - 1 && incl) base = atomicAdd(&sc.n, (unsigned)incl);
             unsigned slot = __builtin_amdgcn_readlane(base, kWave - 1) + (unsigned)(incl - mine);
-            const float gref = gm == -kInf ? 0.f : gm;
-#pragma unroll
-            for (int e = 0; e < G; ++e) {
-                if (x.elem(e) >= L) {
-                    if (slot < kCandCap)
-                        sc.ent[slot] = ((unsigned long long)order_key(x.elem(e)) << 32) | ~(unsigned)(g * G + e);
-                    ++slot;
-                } else {
-                    gs += fast_exp2((x.elem(e) - gref) * a.scale);
-                }
+            for (unsigned left = in; left; left &= left - 1) {       // mostly one
+                const int e = __builtin_ctz(left);
+                if (slot < kCandCap)
+                    sc.ent[slot] = ((unsigned long long)order_key(x.elem_dyn(e)) << 32) | ~(unsigned)(g * G + e);
+                ++slot;
             }
+            RowGroup<BF16> y[1] = {x};
+            leave_out(y[0], in);
+            float gm = -kInf;
+#pragma unroll
+            for (int e = 0; e < G; ++e) gm = fmaxf(gm, y[0].elem(e));
+            const float gs = sum_exp<1>(y, ExpRef(gm, a.scale));
             merge_ms(m, s, gm, gs, a.scale);
         }
     }
