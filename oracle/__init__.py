@@ -24,6 +24,9 @@ Sources (cited by page title and section):
 * "投机解码 Speculative Decoding" tutorial: E(gamma) (section 2.3), the
   temperature division (section 3.3).
 
+``oracle.logits`` holds the logits operators around a round (adjustments,
+a teacher's record, the distillation loss and its gradient).
+
 Parity status of each function is listed in its module header.
 """
 

@@ -10,9 +10,10 @@
 // one byte of its mask.
 //
 // Bound by memory: 64 x 6 rows of 128256 bfloat16 logits (205 MB with masks)
-// take 49 us (4.2 TB/s) with penalties, biases and masks, 43 us with
-// penalties alone, 37 us with masks alone, which is the rate of a copy; the
-// difference is the arithmetic of the waves that hold used tokens.  Masks in
+// take 44 us (4.7 TB/s) with penalties, biases and masks, 39.5 us with
+// penalties alone, 37.5 us with masks alone, which is the rate of a copy; the
+// difference is the chain of loads before the first logit can be written
+// (penalties, seen bits, counts) and the arithmetic of used tokens.  Masks in
 // place on 32 x 6 rows of 152064 (58 MB written): 12 us.  One row of 32000:
 // 4 us, a launch.
 
@@ -160,9 +161,9 @@ __device__ inline float divide(float x, float d, float inv) {
 
 // kAhead positions are loaded at once (mask bytes first: a group of which the
 // mask leaves nothing is not read); four at once take 65 registers, a
-// workgroup per CU less, and 53 us instead of 49.  In place only the groups
+// workgroup per CU less, and 8 % more time.  In place only the groups
 // that change are read and written.  Stores go past the caches (64 x 6 rows:
-// 64 us without).  Eight workgroups per CU in bfloat16; the float32 copy of
+// 6 % more time without).  Eight workgroups per CU in bfloat16; the float32 copy of
 // the kernel would spill at that and is given one less.
 template <bool BF16, bool INPLACE>
 __global__ __launch_bounds__(kBlock, BF16 ? 8 : 7) void k_adjust(AdjustArgs a) {

@@ -16,9 +16,9 @@
 namespace specv {
 namespace {
 
-// Threads per row.  384 rows of 128256 bfloat16 logits, K 64 / 256: 29 / 39 us;
-// with 1024 threads 31 / 50 (longer joins), with 256 29 / 686 (too few maxima
-// to bound 256 candidates by).
+// Threads per row.  384 rows of 128256 bfloat16 logits, K 64 / 256: 28.5 / 35.7
+// us; with 1024 threads 32.0 / 38.6 (longer joins), with 256 28.1 / 414 (too
+// few maxima to bound 256 candidates by).
 constexpr int NT = 512;
 constexpr int NW = NT / kWave;
 constexpr int kBins = 2048;                     // 11-bit digits of the radix select (the last one 10 bits)
@@ -26,7 +26,8 @@ constexpr int kLoads = 4;                       // 16-byte groups a thread loads
 constexpr int kMaxBlocks = 8;                   // blocks per thread (their statistics stand in LDS)
 constexpr int kWaveBlk = 128;                   // blocks a wave reads again
 constexpr int kCandCap = 1024;                  // candidates ranked
-constexpr int kSortFrom = 192;                  // by sorted lists when there are more than this
+constexpr int kSortFrom = 192;                  // by sorted lists when there are more than this: by counting
+                                                // 336 take 6.2 us a row, by lists 280 take 3.2
 constexpr unsigned kLowestFinite = 0x00800000u; // the order key of -FLT_MAX; -inf lies below
 
 // Order key of a logit: larger key, larger value; -0 counts as +0.
