@@ -101,7 +101,7 @@ def _setup(seed, B, n, V, dtype, pos0=0, S=None, used=20):
     return z, h, (rep, pres, freq, slot), drafts, bias, allowed
 
 
-SHAPES = [(1, 1, 1, 0), (2, 3, 7, 0), (3, 2, 8, 1), (2, 4, 33, 2), (2, 6, 2047, 0), (3, 1, 2049, 4), (2, 3, 5001, 0),
+SHAPES = [(1, 2, 2048, 0), (2, 3, 2056, 0), (1, 5, 4096, 3), (1, 32, 65, 31), (300, 2, 2050, 0), (1, 1, 1, 0), (2, 3, 7, 0), (3, 2, 8, 1), (2, 4, 33, 2), (2, 6, 2047, 0), (3, 1, 2049, 4), (2, 3, 5001, 0),
           (2, 32, 129, 0), (2, 2, 131, 30)]
 
 
@@ -190,6 +190,11 @@ def test_strides_broadcasts_and_slots(gpu):
             outside = torch.ones_like(wide, dtype=torch.bool)
             torch.as_strided(outside, shape, strides, off).fill_(False)
             assert torch.equal(wide[outside], keep[outside])           # nothing behind the rows is written
+        W = full_mask.shape[2]
+        padded = torch.full((n, B, W + 5), -1, dtype=torch.int32, device="cuda")     # mask rows apart, other order
+        padded[:, :, 2:2 + W] = full_mask.transpose(0, 1)
+        got = v.adjust_logits(z.cuda(), mask=padded.transpose(0, 1)[:, :, 2:2 + W], **kw)
+        assert torch.equal(got, want)
         one = z[:1, :1].cuda().expand(B, n, V)                         # broadcast logits and mask
         m1 = full_mask[1:2, :1].expand(B, n, -1)
         got = v.adjust_logits(one, mask=m1, **kw)

@@ -192,6 +192,21 @@ def test_against_the_oracle(gpu, dtype, tail, B, n, V, K, T):
     _run(s, _record(t, K, T), w, T, tail)
 
 
+EDGES = [4095, 4096, 4097, 8192, 8200, 16384, 16385, 32767, 32768, 32776, 32777, 49152, 49153, 65536, 65537, 73729,
+         98304, 98305, 131072, 131073]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", EDGES)
+def test_sizes_at_the_edges(gpu, dtype, V):
+    """Lengths where groups, held groups, streamed steps and parts end."""
+    t, s = _rows(V, 1, 2, V, dtype)
+    rec = _record(t, 9, 1.0)
+    rec["tokens"][0, 1, 0] = V - 1                                  # the last token, whatever it holds
+    rec["tokens"][0, 1, 1] = 0
+    _run(s, rec, None, 1.0, "bucket")
+
+
 @pytest.mark.parametrize("tail", ["bucket", "renorm"])
 def test_weights_left_out_and_one_row_alike(gpu, tail):
     t, s = _rows(3, 2, 3, 3001, "bf16")

@@ -68,6 +68,19 @@ def test_normal_rows(gpu, dtype, B, n, V, K, T):
     _run(z, K, T)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [63, 64, 511, 512, 513, 4095, 4096, 4104, 8192, 8193, 16383, 16384, 16385, 65536, 65537,
+                               131071, 131072, 131073, 262144, 262145])
+def test_sizes_at_the_edges(gpu, dtype, V):
+    """Lengths where groups, steps and blocks end; the largest at both ends."""
+    rng = np.random.default_rng(V)
+    z = rng.normal(0, 3, (1, 2, V)).astype(np.float32)
+    z[0, 1, 0] = z[0, 1, V - 1] = 30.0
+    z = torch.from_numpy(z).to(DTYPES[dtype])
+    for K in (2, 40):
+        _run(z, K)
+
+
 def _pattern(name, V, rng):
     z = rng.normal(0, 2, V).astype(np.float32)
     if name == "constant":
