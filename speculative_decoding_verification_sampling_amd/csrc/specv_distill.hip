@@ -84,6 +84,25 @@ __device__ inline void finish_entries(const DistillArgs& a, Entries& r) {
     }
 }
 
+// Of entries with one token the first alone stands for it, whichever of them an
+// atomic has picked: sums over S then run in one order.  (Records rarely hold
+// a token twice; one wave.)
+__device__ inline void first_stands(const DistillArgs& a, const Entries& r, int (&rep)[kE]) {
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int u = 0; u < kE; ++u) rep[u] = r.tok[u] >= 0;
+#pragma unroll
+    for (int q = 0; q < kE; ++q) {
+        const int left = min(kWave, a.K - q * kWave);
+        for (int l = 0; l < left; ++l) {
+            const int t = __builtin_amdgcn_readlane(r.tok[q], l);
+#pragma unroll
+            for (int u = 0; u < kE; ++u)
+                if (r.tok[u] == t && u * kWave + lane > q * kWave + l) rep[u] = 0;
+        }
+    }
+}
+
 // The student's logits of the entries whose token lies in [v0, v1), -inf for
 // the others: all loads first, so that they wait once.
 template <bool BF16>
@@ -269,19 +288,28 @@ __global__ __launch_bounds__(NT, MW) void k_distill(DistillArgs a) {
     float z[kE];
     if (wave == 0) {
         finish_entries(a, r);
+        int rep[kE];
+        bool twice = false;
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            rep[u] = 0;
+            if (r.tok[u] >= 0) {
+                const unsigned bit = 1u << (r.tok[u] % 32);
+                rep[u] = !(atomicOr(&inside[r.tok[u] / 32], bit) & bit);
+                twice |= !rep[u];
+            }
+        }
+        if (__ballot(twice)) {
+            first_stands(a, r, rep);
+            if (lane == 0) sc.twice = 1;
+        }
 #pragma unroll
         for (int u = 0; u < kE; ++u) {
             const int k = lane + u * kWave;
             if (k >= a.K) continue;
-            int rep = 0;
-            if (r.tok[u] >= 0) {
-                const unsigned bit = 1u << (r.tok[u] % 32);
-                rep = !(atomicOr(&inside[r.tok[u] / 32], bit) & bit);
-                if (!rep) sc.twice = 1;
-            }
             sc.tok[k] = r.tok[u];
             sc.t[k] = r.t[u];
-            sc.rep[k] = rep;
+            sc.rep[k] = rep[u];
         }
         load_logits<BF16>(row, r, 0, a.V, z);
 #pragma unroll
@@ -456,15 +484,26 @@ __global__ __launch_bounds__(kBlock) void k_part_stats(DistillArgs a, bool skip)
         finish_entries(a, r);
         float x[kE];
         load_logits<BF16>(row, r, v0, v1, x);
+        int rep[kE];
+        bool twice = false;
+#pragma unroll
+        for (int u = 0; u < kE; ++u) {
+            const int t = r.tok[u];
+            rep[u] = 0;
+            if (t >= v0 && t < v1) {
+                const unsigned bit = 1u << (t % 32);
+                rep[u] = !(atomicOr(&mark[(t - v0) / 32], bit) & bit);
+                twice |= !rep[u];
+            }
+        }
+        if (__ballot(twice)) first_stands(a, r, rep);
 #pragma unroll
         for (int u = 0; u < kE; ++u) {
             const int k = lane + u * kWave, t = r.tok[u];
             if (k >= a.K) continue;
             if (t >= v0 && t < v1) {
-                const unsigned bit = 1u << (t % 32);
-                const bool rep = !(atomicOr(&mark[(t - v0) / 32], bit) & bit);
                 z[k] = x[u];
-                z[a.K + k] = rep ? 1.f : 0.f;
+                z[a.K + k] = rep[u] ? 1.f : 0.f;
             } else if (t < 0 && part == 0) {
                 z[k] = -kInf;
                 z[a.K + k] = 0.f;
