@@ -245,7 +245,8 @@ def test_large_offsets(gpu):
 
 def test_history_against_numpy(gpu):
     rng = np.random.default_rng(21)
-    for B, n, V, S in ((1, 1, 1, 1), (3, 7, 31, 4), (5, 300, 1000, 3), (2, 5000, 257, 2)):
+    for B, n, V, S in ((1, 1, 1, 1), (3, 7, 31, 4), (5, 300, 1000, 3), (2, 5000, 257, 2), (3, 511, 70000, 2),
+                       (3, 512, 70000, 2), (2, 40000, 300000, 2), (2, 33000, 524288, 2), (3, 16385, 3, 2)):
         h = sv.TokenHistory(S, V)
         slots = rng.integers(-1, S + 1, B).astype(np.int32)             # the same slot twice, slots outside
         tok = rng.integers(-2, V + 2, (B, n)).astype(np.int32)
