@@ -34,7 +34,7 @@ constexpr int kAdjChunk = kBlock * kTok;       // tokens per workgroup
 
 constexpr int kHistBlock = 512;                // threads of a workgroup that gathers bits, and its tokens
 constexpr int kHistSpan = 16384, kHistSpanCounted = 1024;
-constexpr int kHistFrom = 512;                 // row length from which it does
+constexpr int kHistFrom = 512;                 // row length from which it does (below, both take a launch)
 
 // 8 logits as they are stored.
 template <bool BF16>

@@ -739,6 +739,13 @@ constexpr long long kPartRows = 64;
 // back to back: 24.4 us, 27.8 with it.
 constexpr long long kPastBytes = 256ll << 20;
 
+// Threads by a row's 16-byte groups: four a thread or so, or the joins of idle
+// waves cost more than the row (2048 rows, bfloat16, us with 256 / 512 / 1024
+// threads: loss and gradient of 1000 groups 18.4 / 23.6 / 38.9, of 1500
+// 23.5 / 26.0 / 40.2 and for 16 rows 7.2 / 6.1 / 7.9, of 3000 40.2 / 37.6 /
+// 45.4, of 4000 55.6 / 54.2 / 54.7 and for 16 rows 12.9 / 9.2 / 8.4; the loss
+// of 1000 groups 12.3 / 18.1, of 2000 19.3 / 21.0 and for 16 rows 5.9 / 5.0).
+// Float32 rows of up to 16 groups a thread are held whole, longer ones by 18.
 template <bool BF16, int OP, bool PAST>
 hipError_t launch_rows(const DistillArgs& a, hipStream_t stream, hipEvent_t* ev) {
     constexpr int G = RowGroup<BF16>::G;
@@ -753,6 +760,7 @@ hipError_t launch_rows(const DistillArgs& a, hipStream_t stream, hipEvent_t* ev)
     else {
 #define SPECV_ROWS(NT, NG, LD, MW) launch(k_distill<BF16, NT, NG, LD, MW, OP, PAST>, rows, NT, lds, stream, ev, a)
         if (full <= 4 * 256) return SPECV_ROWS(256, 4, 2, 8);
+        if (full <= 6 * 512) return SPECV_ROWS(512, 4, 2, 8);
         if (full <= 4 * 1024) return SPECV_ROWS(1024, 4, 2, 8);
         if constexpr (BF16) return SPECV_ROWS(1024, 6, 2, 8);
         else return full <= 16 * 1024 ? SPECV_ROWS(1024, 16, 4, 4) : SPECV_ROWS(1024, 18, 4, 4);
